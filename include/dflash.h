@@ -619,6 +619,142 @@ int df_moe_ffn(const df_mtp_config *cfg, const df_mtp_weights *w, const float *x
                float *out, int32_t *expert_ids, float *expert_w, void *ws, size_t ws_bytes,
                int32_t *d_status, df_stream_t stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Paged KV cache held in 4 bits (no counterpart on the pages, whose cache is contiguous F32:
+ * mtp.rs `MtpKvSlot`). A sequence's row p lives in row p % page_size of page
+ * page_table[b, p / page_size]; the pages of all sequences share one pool, so a sequence takes
+ * memory as it grows and an F32 row of d values takes 9 d / 16 bytes.
+ *
+ * A row of one KV head is d / 16 blocks of 16 consecutive dims. With y the row's values divided
+ * by the cache's k_scale or v_scale, a block holds
+ *   the scale s = e4m3(max|y| / 6)   (8 bits, nearest, ties to even, at most 448)
+ *   16 codes  c = e2m1(y / s)        (4 bits, one of 0, .5, 1, 1.5, 2, 3, 4, 6 and a sign,
+ *                                     nearest, ties to the even code, at most 6; 0 when s = 0)
+ * and stands for c * s * k_scale (v_scale). Dim 2i is the low half of byte i, dim 2i + 1 the high
+ * half. Scales and codes are those of the real-number definition: values within rounding error
+ * of a boundary are decided in float64.
+ * One struct describes one layer; the page table and the lengths may be shared by the layers.
+ * ---------------------------------------------------------------------------------------- */
+typedef struct {
+    uint8_t *k_codes, *v_codes;    /* device [n_pages, n_kv_heads, page_size, head_dim / 2],
+                                      16-byte aligned */
+    uint8_t *k_scales, *v_scales;  /* device [n_pages, n_kv_heads, page_size, head_dim / 16],
+                                      16-byte aligned */
+    const int32_t *page_table;     /* device [batch, max_pages]: page ids in [0, n_pages); entries
+                                      past a sequence's rows are not read */
+    const int32_t *seq_len;        /* device [batch]: valid rows of every sequence */
+    int32_t n_pages, page_size;    /* page_size 16, 32, 64, 128 or 256 */
+    int32_t max_pages;             /* page table entries per sequence */
+    int32_t batch;                 /* at most 4096 */
+    int32_t n_kv_heads, head_dim;  /* head_dim 64, 128 or 256 */
+    float k_scale, v_scale;        /* powers of two (1 unless the values need another range) */
+} df_paged_kv;
+
+/* Rotary positions of the new rows: pair i (dims i and i + rotary_dim / 2) of a head turns by
+ * position * inv_freq[i], the position taken on the axis of the pair. */
+typedef struct {
+    const double *inv_freq;     /* device F64 [rotary_dim / 2], e.g. theta^(-2i / rotary_dim) */
+    const int32_t *positions;   /* device [n_axes, batch, n_max], or NULL: row i of sequence b is at
+                                   position seq_len[b] + i on every axis */
+    const uint8_t *axis;        /* device [rotary_dim / 2]: the axis of every pair, in
+                                   [0, n_axes), or NULL: axis 0 */
+    int32_t rotary_dim;         /* a multiple of 16, at most head_dim */
+    int32_t n_axes;             /* 1..4 (time, height, width of pictures and video, ...) */
+} df_rope;
+
+/*
+ * df_kv_append_paged — the new rows of every sequence, in one launch: per-head RMSNorm of q and k,
+ * rotary positions on q and k, and k and v appended to the cache (the paged form of the step
+ * between the QKV projection and the attention; mtp.rs `forward_full_attention`).
+ *   q, k, v    device F32, 16-byte aligned: row (b, i) at (b * n_max + i) * ldq (ldk, ldv), then
+ *              [heads, head_dim]; ld* multiples of 4, so one projection's q | k | v rows can be
+ *              passed as they are. q may be NULL (n_q_heads 0).
+ *   q_norm, k_norm  device F32 [head_dim], or NULL: no norm. eps >= 0.
+ *   rope       HOST struct, or NULL: no rotation
+ *   n_new      device int32 [batch], each in [0, n_max], or NULL: n_max rows each
+ *   q_out      device F32 [batch, n_max, n_q_heads, head_dim] out, 16-byte aligned (NULL with
+ *              q): normed and rotated q
+ * Row i < n_new[b] is stored as cache row seq_len[b] + i; the others are neither read nor written
+ * (in q_out as in the cache). seq_len is not changed: the layers of a step append at the same
+ * rows, then kv_advance moves it. Rows to append must not be shared by two sequences.
+ * Device status: DF_ESHAPE (n_new out of range, clamped), DF_ECAPACITY (row past max_pages pages,
+ * skipped; a negative seq_len), DF_EINVAL (page id outside [0, n_pages), skipped; an axis
+ * outside [0, n_axes), taken as 0; a k or v that is not finite once normed and rotated: infinities
+ * saturate, NaN is stored as 0).
+ */
+int df_kv_append_paged(const df_paged_kv *cache, const float *q, int ldq, int n_q_heads,
+                       const float *k, int ldk, const float *v, int ldv, const float *q_norm,
+                       const float *k_norm, float eps, const df_rope *rope, const int32_t *n_new,
+                       int n_max, float *q_out, int32_t *d_status, df_stream_t stream);
+
+/*
+ * df_kv_gather_paged — rows of every sequence as the F32 values they stand for, in the contiguous
+ * layout that df_attention reads.
+ *   start   device int32 [batch] (or NULL: 0): first row of every sequence
+ *   n       device int32 [batch], each in [0, n_max], or NULL: n_max rows each
+ *   k_out, v_out   device F32 [batch, n_kv_heads, n_max, head_dim] out, 16-byte aligned
+ * Rows i >= n[b] of the outputs are left as they were. Any row of the page table's capacity may
+ * be read, whatever seq_len says. Device status as df_kv_append_paged (a skipped row is left).
+ */
+int df_kv_gather_paged(const df_paged_kv *cache, const int32_t *start, const int32_t *n, int n_max,
+                       float *k_out, float *v_out, int32_t *d_status, df_stream_t stream);
+
+/* kv_advance — the counterpart of kv_rollback: seq_len[b] += n[b], once the rows of a step have
+ * been appended. n[b] < 0, or a length above cap, is clamped and DF_ECAPACITY written. */
+int kv_advance(int32_t *seq_len, const int32_t *n, int B, int cap, int32_t *d_status,
+               df_stream_t stream);
+
+/*
+ * df_attention_paged — attention over a paged 4-bit cache: softmax(q k^T / sqrt(d)) v with grouped
+ * KV heads, for single tokens, for blocks of drafts and for pieces of a prompt.
+ *   q        device F32 [batch, blk, nq, head_dim], 16-byte aligned (as df_kv_append_paged's q_out)
+ *   n_new    device int32 [batch], each in [0, blk], or NULL. Given: row i < n_new[b] is the query
+ *            of cache row seq_len[b] + i, the keys are the rows below seq_len[b] + n_new[b], and
+ *            the rows i >= n_new[b] of out are left as they were. NULL: blk rows, the keys are
+ *            the rows below seq_len[b].
+ *   causal   1 (n_new given): row i sees the rows up to its own, seq_len[b] + i; 0: every row
+ *            sees all the keys
+ *   out      device F32 [batch, blk, nq, head_dim] out, 16-byte aligned
+ * Query head h reads KV head h / (nq / n_kv_heads). A row with no visible key gets zeros. q
+ * enters the tensor cores as a pair of FP16 values (about 22 bits below the row's largest), the
+ * cached values exactly; the probabilities as a pair too; sums are F32. A value that is not finite
+ * in a row of q reaches that row of out alone.
+ * The workspace (allocated zeroed) holds the partial results of keys that several CTAs share.
+ * Device status: DF_ESHAPE (n_new out of range), DF_ECAPACITY (more keys than the table's pages;
+ * a negative length), both clamped; DF_EINVAL (page id outside [0, n_pages); its rows count as
+ * zeros).
+ */
+size_t df_attention_paged_workspace_bytes(const df_paged_kv *cache, int blk, int nq);
+int df_attention_paged(const df_paged_kv *cache, const float *q, const int32_t *n_new, int blk,
+                       int nq, int causal, float *out, void *ws, size_t ws_bytes,
+                       int32_t *d_status, df_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Log probabilities of given tokens, with the entropy and the top alternatives of every row: what
+ * a serving loop reports beside the tokens that sample_softmax or the accept step chose. With
+ * z = logits[r] / T, M = max z and S = sum of e^(z - M) over all entries but one that is M:
+ *   logprob[r] = z[token] - M - log1p(S)
+ *   entropy[r] = log1p(S) + (sum of (M - z) e^(z - M)) / (1 + S)        (in nats)
+ *   top_ids, top_logprobs: the top_k entries of largest z, the lower index first among equals
+ * so that a near-certain row keeps its relative accuracy. Entries of -inf are probabilities of 0.
+ * ---------------------------------------------------------------------------------------- */
+/* Workspace (allocate it zeroed); 0 for unsupported sizes. */
+size_t df_token_logprobs_workspace_bytes(int R, int V, int top_k);
+
+/*   logits       device [R, V], row r at r * ld elements (ld >= V); F32 (logits_bf16 = 0) or BF16
+ *                (1) bit patterns, aligned to the element
+ *   temperature  > 0 (DF_EINVAL otherwise)
+ *   tokens       device int32 [R]; -1: no token (logprob 0). Others outside [0, V): logprob NaN
+ *                and DF_EINVAL in d_status
+ *   logprob      device F32 [R] out; entropy device F32 [R] out, or NULL
+ *   top_k        0..32 and at most V; top_ids device int32 [R, top_k] out and top_logprobs device
+ *                F32 [R, top_k] out (NULL when top_k = 0)
+ * A row with a NaN, a +inf or nothing but -inf gets NaN results and sets DF_EINVAL in d_status. */
+int df_token_logprobs(const void *logits, int logits_bf16, int R, int V, long long ld,
+                      float temperature, const int32_t *tokens, float *logprob, float *entropy,
+                      int top_k, int32_t *top_ids, float *top_logprobs, void *ws, size_t ws_bytes,
+                      int32_t *d_status, df_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,88 @@
+"""Plain float64 restatement of the paged 4-bit KV cache and of the token log probabilities:
+number formats by table, rows one at a time."""
+from __future__ import annotations
+
+import numpy as np
+
+E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+# every finite non-negative E4M3 value, in the order of its bit pattern
+E4M3 = np.array([m / 8 * 2.0 ** -6 for m in range(8)]
+                + [(1 + m / 8) * 2.0 ** (e - 7) for e in range(1, 16) for m in range(8)])[:127]
+
+
+def nearest(values, x):
+    """Index of the nearest of sorted `values` to every x >= 0; ties go to the even index."""
+    x = np.minimum(np.asarray(x, dtype=np.float64), values[-1])
+    hi = np.clip(np.searchsorted(values, x), 1, len(values) - 1)
+    lo = hi - 1
+    down, up = x - values[lo], values[hi] - x
+    return np.where((up < down) | ((up == down) & (hi % 2 == 0)), hi, lo)
+
+
+def quantise(y, scale=1.0):
+    """Codes [..., d] (sign in bit 3) and scale patterns [..., d / 16] of float64 rows y."""
+    y = np.asarray(y, dtype=np.float64) / scale
+    t = y.reshape(*y.shape[:-1], -1, 16)
+    s = nearest(E4M3, np.abs(t).max(-1) / 6)
+    sv = E4M3[s][..., None]
+    c = nearest(E2M1, np.where(sv > 0, np.abs(t) / np.where(sv > 0, sv, 1), 0.0))
+    c = c | (np.signbit(t).astype(np.int64) << 3)
+    return c.reshape(y.shape).astype(np.uint8), s.astype(np.uint8)
+
+
+def values(codes, scales, scale=1.0):
+    """What codes [..., d] and scale patterns [..., d / 16] stand for (float64)."""
+    c = codes.astype(np.int64)
+    v = E2M1[c & 7] * np.where(c & 8, -1.0, 1.0)
+    return v * np.repeat(E4M3[scales.astype(np.int64)], 16, axis=-1) * scale
+
+
+def pack(codes):
+    return (codes[..., 0::2] | (codes[..., 1::2] << 4)).astype(np.uint8)
+
+
+def unpack(b):
+    return np.stack((b & 15, b >> 4), -1).reshape(*b.shape[:-1], 2 * b.shape[-1])
+
+
+def norm_rope(x, w, eps, inv_freq, pos):
+    """Per-head RMSNorm (w None: none) and rotation of rows x [n, heads, d]; pos [n, rot / 2] are
+    the positions of every pair (None: no rotation)."""
+    y = np.asarray(x, dtype=np.float64)
+    if w is not None:
+        y = y / np.sqrt((y * y).mean(-1, keepdims=True) + eps) * np.asarray(w, dtype=np.float64)
+    if pos is not None:
+        h = len(inv_freq)
+        a = np.asarray(pos, dtype=np.float64) * np.asarray(inv_freq, dtype=np.float64)
+        c, s = np.cos(a)[:, None], np.sin(a)[:, None]
+        y = np.concatenate((y[..., :h] * c - y[..., h:2 * h] * s, y[..., h:2 * h] * c + y[..., :h] * s,
+                            y[..., 2 * h:]), -1)
+    return y
+
+
+def attention(q, k, v, limit):
+    """q [rows, heads, d], k / v [keys, kv heads, d], limit [rows]: keys row i sees. Float64."""
+    rows, nq, d = q.shape
+    out = np.zeros((rows, nq, d))
+    g = nq // k.shape[1]
+    for i in range(rows):
+        n = int(limit[i])
+        if n <= 0:
+            continue
+        for h in range(nq):
+            x = k[:n, h // g] @ q[i, h].astype(np.float64) / np.sqrt(d)
+            p = np.exp(x - x.max())
+            out[i, h] = (p[:, None] * v[:n, h // g]).sum(0) / p.sum()
+    return out
+
+
+def logprobs(x, T, token, top):
+    """(log probability, entropy, top ids, top log probabilities) of one row."""
+    z = np.asarray(x, dtype=np.float64) / T
+    j = int(np.argmax(z))
+    e = np.exp(z - z[j])
+    rest = np.delete(e, j).sum()
+    ls = np.log1p(rest)
+    d = np.where(e > 0, z - z[j], 0.0)
+    order = np.lexsort((np.arange(len(z)), -z))[:top]
+    return z[token] - z[j] - ls, ls - (e * d).sum() / (1 + rest), order, z[order] - z[j] - ls

@@ -74,6 +74,19 @@ class MtpWeights(ctypes.Structure):
         "sh_gate_mlp", "sh_up", "sh_down", "sh_expert_gate", "tiled")]
 
 
+class PagedKvC(ctypes.Structure):
+    _fields_ = [("k_codes", c_void_p), ("v_codes", c_void_p), ("k_scales", c_void_p),
+                ("v_scales", c_void_p), ("page_table", c_void_p), ("seq_len", c_void_p),
+                ("n_pages", c_int32), ("page_size", c_int32), ("max_pages", c_int32),
+                ("batch", c_int32), ("n_kv_heads", c_int32), ("head_dim", c_int32),
+                ("k_scale", c_float), ("v_scale", c_float)]
+
+
+class RopeC(ctypes.Structure):
+    _fields_ = [("inv_freq", c_void_p), ("positions", c_void_p), ("axis", c_void_p),
+                ("rotary_dim", c_int32), ("n_axes", c_int32)]
+
+
 _lib = None
 
 # (name, restype, argtypes)
@@ -160,6 +173,19 @@ _SIGS = [
     ("df_moe_workspace_bytes", c_size_t, [POINTER(MtpConfig), c_int]),
     ("df_moe_ffn", c_int, [POINTER(MtpConfig), POINTER(MtpWeights), c_void_p, c_int, c_void_p,
                            c_void_p, c_void_p, c_void_p, c_size_t, c_void_p, c_void_p]),
+    ("df_kv_append_paged", c_int, [POINTER(PagedKvC), c_void_p, c_int, c_int, c_void_p, c_int,
+                                   c_void_p, c_int, c_void_p, c_void_p, c_float, POINTER(RopeC),
+                                   c_void_p, c_int, c_void_p, c_void_p, c_void_p]),
+    ("df_kv_gather_paged", c_int, [POINTER(PagedKvC), c_void_p, c_void_p, c_int, c_void_p, c_void_p,
+                                   c_void_p, c_void_p]),
+    ("kv_advance", c_int, [c_void_p, c_void_p, c_int, c_int, c_void_p, c_void_p]),
+    ("df_attention_paged_workspace_bytes", c_size_t, [POINTER(PagedKvC), c_int, c_int]),
+    ("df_attention_paged", c_int, [POINTER(PagedKvC), c_void_p, c_void_p, c_int, c_int, c_int,
+                                   c_void_p, c_void_p, c_size_t, c_void_p, c_void_p]),
+    ("df_token_logprobs_workspace_bytes", c_size_t, [c_int, c_int, c_int]),
+    ("df_token_logprobs", c_int, [c_void_p, c_int, c_int, c_int, ctypes.c_longlong, c_float, c_void_p,
+                                  c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_size_t,
+                                  c_void_p, c_void_p]),
 ]
 
 
@@ -658,3 +684,188 @@ def generate(model: "DFlashModel", ref, agree, table, sel, prior_cap, prior_len,
                              max_new_tokens, max_rounds, B, K, n_new_max, _p(eos), n_eos,
                              _p(rounds), _p(accept_hist), _p(ws), ws.numel(), _p(d_status),
                              _stream(stream)))
+
+
+# ----------------------------------------------------------------------------- paged 4-bit cache
+U8, F64 = torch.uint8, torch.float64
+
+
+def _same_device(cache, *tensors):
+    """The calls below run on the cache's device, on that device's current stream: a tensor of
+    another device raises here."""
+    for t in tensors:
+        if t is not None and t.device != cache.device:
+            raise ValueError(f"a tensor on {t.device}, the first on {cache.device}")
+
+
+def _run(device, stream, fn, *args):
+    """fn(*args, stream) with `device` current (the library launches on the current device)."""
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream(stream)))
+
+
+class PagedKv:
+    """One layer's paged 4-bit KV cache (df_paged_kv): codes [pages, kv heads, page, d / 2] and
+    scales [pages, kv heads, page, d / 16], both uint8, for k and v; page_table [B, max pages] and
+    seq_len [B] int32. Keeps the tensors alive."""
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales, page_table, seq_len,
+                 k_scale: float = 1.0, v_scale: float = 1.0):
+        n_pages, n_kv, page, half = k_codes.shape
+        B, max_pages = page_table.shape
+        if (k_codes.shape != v_codes.shape or k_scales.shape != v_scales.shape
+                or tuple(k_scales.shape) != (n_pages, n_kv, page, half // 8)
+                or tuple(seq_len.shape) != (B,)):
+            raise ValueError("codes [pages, kv, page, d / 2], scales [pages, kv, page, d / 16], "
+                             "page_table [B, max pages] and seq_len [B] do not fit together")
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = (k_codes, k_scales, v_codes,
+                                                                    v_scales)
+        self.page_table, self.seq_len = page_table, seq_len
+        self.device = k_codes.device
+        self.batch, self.n_kv, self.head_dim = B, n_kv, 2 * half
+        self.cap = max_pages * page
+        self.c = PagedKvC(_dev(k_codes, U8, "k_codes"), _dev(v_codes, U8, "v_codes"),
+                          _dev(k_scales, U8, "k_scales"), _dev(v_scales, U8, "v_scales"),
+                          _dev(page_table, I32, "page_table"), _dev(seq_len, I32, "seq_len"),
+                          n_pages, page, max_pages, B, n_kv, 2 * half, k_scale, v_scale)
+        self.ref = ctypes.byref(self.c)
+        _same_device(self, k_scales, v_codes, v_scales, page_table, seq_len)
+
+    @classmethod
+    def empty(cls, n_pages: int, page_size: int, n_kv: int, head_dim: int, page_table, seq_len,
+              k_scale: float = 1.0, v_scale: float = 1.0):
+        """A cache with pools of its own (zeros), on the page table's device."""
+        z = dict(dtype=U8, device=page_table.device)
+        pools = [torch.zeros((n_pages, n_kv, page_size, head_dim // n), **z) for n in (2, 16, 2, 16)]
+        return cls(*pools, page_table, seq_len, k_scale, v_scale)
+
+
+def rope_frequencies(theta: float, rotary_dim: int, device="cuda") -> torch.Tensor:
+    """theta^(-2i / rotary_dim), i < rotary_dim / 2, float64: the inv_freq of kv_append_paged."""
+    i = torch.arange(rotary_dim // 2, dtype=F64)
+    return (float(theta) ** (-2.0 * i / rotary_dim)).to(device)
+
+
+def _rows(t, B: int, n_max: int, width: int, name: str):
+    """Pointer and row stride of [B, n_max, width] F32 rows that may be part of wider ones."""
+    if t is None:
+        return None, 0
+    if not t.is_cuda or t.dtype != F32 or tuple(t.shape) != (B, n_max, width):
+        raise TypeError(f"{name}: expected a CUDA {F32} tensor [{B}, {n_max}, {width}], got "
+                        f"{t.dtype} {list(t.shape)} on {t.device}")
+    ld = t.stride(1) if n_max > 1 else (t.stride(0) if B > 1 else max(t.stride(1), width))
+    if (width > 1 and t.stride(2) != 1) or (B > 1 and t.stride(0) != n_max * ld):
+        raise TypeError(f"{name}: rows must be evenly spaced with unit stride inside, got strides "
+                        f"{t.stride()}")
+    return t.data_ptr(), ld
+
+
+def kv_append_paged(cache: PagedKv, q, k, v, q_out=None, n_new=None, q_norm=None, k_norm=None,
+                    eps: float = 1e-6, inv_freq=None, positions=None, axis=None, d_status=None,
+                    stream=None):
+    """Norms, rotary positions and the append of new rows (df_kv_append_paged). q [B, n, nq * d] or
+    None, k and v [B, n, n_kv * d] (each may be a slice of one projection's rows); q_out
+    [B, n, nq, d]; n_new [B] int32 or None; inv_freq [rot / 2] float64 or None (no rotation);
+    positions [axes, B, n] int32 or None; axis [rot / 2] uint8 or None."""
+    B, n_max = k.shape[0], k.shape[1]
+    d = cache.head_dim
+    if B != cache.batch:
+        raise ValueError(f"k has {B} sequences, the cache {cache.batch}")
+    nq = 0 if q is None else q.shape[2] // d
+    qp, ldq = _rows(q, B, n_max, nq * d, "q")
+    kp, ldk = _rows(k, B, n_max, cache.n_kv * d, "k")
+    vp, ldv = _rows(v, B, n_max, cache.n_kv * d, "v")
+    if (q is None) != (q_out is None) or (q is not None and tuple(q_out.shape) != (B, n_max, nq, d)):
+        raise ValueError(f"q_out must be [{B}, {n_max}, {nq}, {d}] with q, None without")
+    _sizes("kv_append_paged", (n_new, (B,)), (q_norm, (d,)), (k_norm, (d,)))
+    rope = None
+    if inv_freq is not None:
+        half = inv_freq.shape[0]
+        axes = 1 if positions is None else positions.shape[0]
+        _sizes("kv_append_paged", (positions, (axes, B, n_max)), (axis, (half,)))
+        rope = ctypes.byref(RopeC(_dev(inv_freq, F64, "inv_freq"), _dev(positions, I32, "positions"),
+                                  _dev(axis, U8, "axis"), 2 * half, axes))
+    elif positions is not None or axis is not None:
+        raise ValueError("positions and axis need inv_freq")
+    _same_device(cache, q, k, v, q_out, n_new, q_norm, k_norm, inv_freq, positions, axis, d_status)
+    _run(cache.device, stream, lib().df_kv_append_paged, cache.ref, qp, ldq, nq, kp, ldk, vp, ldv,
+         _dev(q_norm, F32, "q_norm"), _dev(k_norm, F32, "k_norm"), eps, rope,
+         _dev(n_new, I32, "n_new"), n_max, _dev(q_out, F32, "q_out"), _dev(d_status, I32, "d_status"))
+
+
+def _sizes(call: str, *pairs):
+    for t, shape in pairs:
+        if t is not None and tuple(t.shape) != shape:
+            raise ValueError(f"{call}: expected {list(shape)}, got {list(t.shape)}")
+
+
+def kv_gather_paged(cache: PagedKv, n, k_out, v_out, start=None, d_status=None, stream=None):
+    """Cached rows start[b] .. start[b] + n[b] as F32 values (df_kv_gather_paged): k_out, v_out
+    [B, n_kv, n_max, d], the layout df_attention reads; n and start [B] int32 or None."""
+    B, n_max = cache.batch, k_out.shape[2]
+    shape = (B, cache.n_kv, n_max, cache.head_dim)
+    _sizes("kv_gather_paged", (k_out, shape), (v_out, shape), (n, (B,)), (start, (B,)))
+    _same_device(cache, n, k_out, v_out, start, d_status)
+    _run(cache.device, stream, lib().df_kv_gather_paged, cache.ref, _dev(start, I32, "start"),
+         _dev(n, I32, "n"), n_max, _dev(k_out, F32, "k_out"), _dev(v_out, F32, "v_out"),
+         _dev(d_status, I32, "d_status"))
+
+
+def kv_advance(seq_len, n, cap: int, d_status=None, stream=None):
+    """seq_len[b] += n[b], at most cap: after the rows of a step have been appended."""
+    _sizes("kv_advance", (n, tuple(seq_len.shape)))
+    _same_device(seq_len, n, d_status)
+    _run(seq_len.device, stream, lib().kv_advance, _dev(seq_len, I32, "seq_len"), _dev(n, I32, "n"),
+         seq_len.shape[0], cap, _dev(d_status, I32, "d_status"))
+
+
+def attention_paged_workspace_bytes(cache: PagedKv, blk: int, nq: int) -> int:
+    return int(lib().df_attention_paged_workspace_bytes(cache.ref, blk, nq))
+
+
+def attention_paged(cache: PagedKv, q, out, ws, n_new=None, causal: bool = False, d_status=None,
+                    stream=None):
+    """Attention over the paged 4-bit cache (df_attention_paged): q and out [B, blk, nq, d];
+    n_new [B] int32: row i < n_new[b] is the query of cache row seq_len[b] + i; None: blk rows over
+    the seq_len[b] cached ones."""
+    B, blk, nq, d = q.shape
+    if B != cache.batch or d != cache.head_dim:
+        raise ValueError(f"q is {list(q.shape)}, the cache has {cache.batch} sequences and "
+                         f"head_dim {cache.head_dim}")
+    _sizes("attention_paged", (out, (B, blk, nq, d)), (n_new, (B,)))
+    _same_device(cache, q, out, ws, n_new, d_status)
+    _run(cache.device, stream, lib().df_attention_paged, cache.ref, _dev(q, F32, "q"),
+         _dev(n_new, I32, "n_new"), blk, nq, 1 if causal else 0, _dev(out, F32, "out"),
+         _dev(ws, U8, "ws"), ws.numel(), _dev(d_status, I32, "d_status"))
+
+
+# ----------------------------------------------------------------------------- log probabilities
+def token_logprobs_workspace_bytes(R: int, V: int, top_k: int) -> int:
+    return int(lib().df_token_logprobs_workspace_bytes(R, V, top_k))
+
+
+def token_logprobs(logits, tokens, logprob, entropy=None, top_ids=None, top_logprobs=None, ws=None,
+                   temperature: float = 1.0, d_status=None, stream=None):
+    """Log probability of tokens[r] (int32, -1: none), entropy and top alternatives of every row of
+    logits [R, V] (F32 or BF16; rows may be part of wider ones) at a temperature
+    (df_token_logprobs). top_ids / top_logprobs [R, top_k], or both None."""
+    R, V = logits.shape
+    if not logits.is_cuda or logits.dtype not in (F32, BF16) or (V > 1 and logits.stride(1) != 1):
+        raise TypeError(f"logits: expected CUDA {F32} or {BF16} rows with unit stride, got "
+                        f"{logits.dtype} {logits.stride()} on {logits.device}")
+    ld = max(logits.stride(0), V) if R == 1 else logits.stride(0)
+    top_k = 0 if top_ids is None else top_ids.shape[1]
+    _sizes("token_logprobs", (tokens, (R,)), (logprob, (R,)), (entropy, (R,)), (top_ids, (R, top_k)),
+           (top_logprobs, (R, top_k)))
+    if (top_ids is None) != (top_logprobs is None):
+        raise ValueError("top_ids and top_logprobs go together")
+    _same_device(logits, tokens, logprob, entropy, top_ids, top_logprobs, ws, d_status)
+    _run(logits.device, stream, lib().df_token_logprobs, logits.data_ptr(),
+         1 if logits.dtype == BF16 else 0, R, V, ld, temperature, _dev(tokens, I32, "tokens"),
+         _dev(logprob, F32, "logprob"), _dev(entropy, F32, "entropy"), top_k,
+         _dev(top_ids, I32, "top_ids") if top_k else None,
+         _dev(top_logprobs, F32, "top_logprobs") if top_k else None, _dev(ws, U8, "ws"),
+         0 if ws is None else ws.numel(), _dev(d_status, I32, "d_status"))

@@ -28,6 +28,8 @@ int fail(int code, const char *fmt, ...) {
     return code;
 }
 
+void clear_error() { g_err[0] = 0; }
+
 // ---------------------------------------------------------------- launch set-up
 int sm_count() {
     static std::atomic<int> cached[64];

@@ -123,7 +123,7 @@ enum TraceKid : uint32_t {
     TK_LOOP_INIT, TK_LOOP_PREPARE, TK_LOOP_VERIFY, TK_LOOP_APPEND, TK_LOOP_COMMIT, TK_MOE_ROUTER,
     TK_MOE_GATE_UP, TK_MOE_DOWN, TK_PACK, TK_PACK_VEC, TK_ARGMAX_FINAL, TK_ACCEPT, TK_ROLLBACK,
     TK_WORD_COPY, TK_SAMPLE_STATS, TK_SAMPLE_WALK, TK_SAMPLE_NORM, TK_SAMPLE_DRAW,
-    TK_SAMPLE_FUSED, TK_TILE,
+    TK_SAMPLE_FUSED, TK_TILE, TK_KV_APPEND, TK_KV_GATHER, TK_ATTN_PAGED, TK_LOGPROBS,
     TK_GEMM = 100   // + 2 * epilogue + (stream-K fix-up ? 1 : 0)
 };
 struct TraceRec {
@@ -599,6 +599,63 @@ int launch_accept(const int32_t *drafts, int ld, const int32_t *target, int B, i
                   int32_t *accept_count, int32_t *hit_eos, int32_t *rollback,
                   int32_t *target_seq_len, int32_t *status, cudaStream_t s);
 int launch_rollback(int32_t *seq_len, const int32_t *n, int B, int32_t *status, cudaStream_t s);
+
+// Arrival counters of the paged attention (one per CTA) and of the log probabilities (one per row
+// that is cut into chunks): the same few at the start of every workspace, so calls of any sizes
+// may follow each other on one.
+constexpr int kOpsCounters = 4096;
+
+// Paged 4-bit KV cache (k_paged.cu, k_attn_paged.cu).
+constexpr int kPagedMaxBatch = 4096;
+constexpr int kPagedMaxAxes = 4;
+struct KvAppendArgs {
+    df_paged_kv c;
+    const float *q = nullptr, *k = nullptr, *v = nullptr;
+    int ldq = 0, ldk = 0, ldv = 0, nq = 0;
+    const float *q_norm = nullptr, *k_norm = nullptr;
+    float eps = 0.f;
+    df_rope rope;                    // rotary_dim 0: no rotation
+    const int32_t *n_new = nullptr;
+    int n_max = 0;
+    float *q_out = nullptr;
+    int32_t *status = nullptr;
+};
+int launch_kv_append_paged(const KvAppendArgs &a, cudaStream_t s);
+int launch_kv_gather_paged(const df_paged_kv &c, const int32_t *start, const int32_t *n, int n_max,
+                           float *k_out, float *v_out, int32_t *status, cudaStream_t s);
+struct AttnPagedArgs {
+    df_paged_kv c;
+    const float *q = nullptr;        // [B, blk, nq, d]
+    const int32_t *n_new = nullptr;
+    int blk = 0, nq = 0, causal = 0;
+    float *out = nullptr;
+    float *part = nullptr;           // partial results (attn_paged_part_floats)
+    int *counters = nullptr;         // [kOpsCounters], zero between calls
+    int32_t *status = nullptr;
+};
+size_t attn_paged_part_floats(const df_paged_kv &c, int blk, int nq);
+int launch_attn_paged(const AttnPagedArgs &a, cudaStream_t s);
+
+// Log probabilities of given tokens (k_logprobs.cu).
+constexpr int kLogprobsMaxTop = 32;
+struct LogprobsArgs {
+    const void *logits = nullptr;
+    int bf16 = 0, R = 0, V = 0;
+    long long ld = 0;
+    float T = 1.f;
+    const int32_t *tokens = nullptr;
+    float *logprob = nullptr, *entropy = nullptr;
+    int top_k = 0;
+    int32_t *top_ids = nullptr;
+    float *top_lp = nullptr;
+    void *part = nullptr;            // per-chunk states (logprobs_part_bytes)
+    int *counters = nullptr;         // [kOpsCounters], zero between calls
+    int32_t *status = nullptr;
+};
+size_t logprobs_part_bytes(int R, int V);
+int launch_token_logprobs(const LogprobsArgs &a, cudaStream_t s);
+// Empties the thread's error text (the first step of an entry point).
+void clear_error();
 // argmax_final + accept in one launch for blocks of 2..32 rows (one CTA per sequence).
 int launch_argmax_accept(const ArgTop *part, int G, int B, int blk, int32_t *argmax_out,
                          const int32_t *target, const int32_t *eos, int n_eos,

@@ -1,0 +1,436 @@
+// Log probabilities of given tokens, entropy and top alternatives of rows of logits, in one pass.
+//
+// With z = x / T, M = max z and one entry that is M left out of the sum S = sum e^(z - M):
+//   log p_t = z_t - M - log1p(S),  H = log1p(S) + (sum (M - z) e^(z - M)) / (1 + S).
+// Leaving the maximum out keeps S (and with it 1 - p_max) to full relative accuracy however
+// peaked the row is, and every term of H is then non-negative. The top entries are kept apart
+// anyway, so S sums what is not among them and they are added at the end.
+#include <cuda_bf16.h>
+
+#include "df_internal.cuh"
+
+namespace df {
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kPerLane = 16;                 // logits of one lane and step
+constexpr int kStep = 32 * kPerLane;         // logits of one warp and step
+constexpr int kNone = 0x7fffffff;            // index of an empty list entry
+constexpr float kFloor = -150.f;             // exponents below it count as 0 (2^-150 is 0 in F32)
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// max that keeps a NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<unsigned long long &>(r))
+        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)));
+    return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<unsigned long long &>(r))
+        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<unsigned long long &>(r))
+        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)),
+          "l"(reinterpret_cast<unsigned long long &>(c)));
+    return r;
+}
+
+__device__ __forceinline__ bool better(float av, int ai, float bv, int bi) {
+    return av > bv || (av == bv && ai < bi);
+}
+
+// A warp's running state: the best kp entries seen, sorted, one a lane (lanes >= kp are empty),
+// and over all others the lane's sums of e = 2^(c (x - mu)) and of e * log2(e).
+struct State {
+    float lv;
+    int li;
+    float mu, S, U;
+
+    // Entry (v, i) to the sums. (While mu is unset every entry so far is -inf.)
+    __device__ void drop(float v, int i, float c) {
+        if (i == kNone || mu == -INFINITY) return;
+        const float t = max_nan((v - mu) * c, kFloor), e = ex2(t);
+        S += e;
+        U = fmaf(e, t, U);
+    }
+    // Sums restated against m >= every value summed.
+    __device__ void rebase(float m, float c) {
+        if (m == -INFINITY || mu == -INFINITY) {
+            if (S == S) S = U = 0.f;
+        } else if (mu != m) {
+            const float dt = (mu - m) * c, f = ex2(dt);
+            S *= f;
+            U = fmaf(U, f, S == 0.f ? 0.f : dt * S);
+        }
+        mu = m;
+    }
+    // Entry (v, i), the same in every lane, if it is among the best kp; the entry it displaces
+    // goes to lane 0's sums. True if it was taken.
+    __device__ bool insert(float v, int i, int kp, float c) {
+        const int lane = threadIdx.x & 31;
+        const unsigned ahead = __ballot_sync(0xffffffffu, better(lv, li, v, i));
+        const int pos = __popc(ahead);
+        if (pos >= kp) return false;
+        const float ev = __shfl_sync(0xffffffffu, lv, kp - 1), uv = __shfl_up_sync(0xffffffffu, lv, 1);
+        const int ei = __shfl_sync(0xffffffffu, li, kp - 1), ui = __shfl_up_sync(0xffffffffu, li, 1);
+        if (lane >= pos && lane < kp) {
+            lv = lane == pos ? v : uv;
+            li = lane == pos ? i : ui;
+        }
+        if (lane == 0) drop(ev, ei, c);
+        return true;
+    }
+    // The best kp of this list and of (bv, bi), sorted the same way; the rest goes to the sums.
+    __device__ void merge(float bv, int bi, int kp, float c) {
+        const int lane = threadIdx.x & 31;
+        bv = __shfl_sync(0xffffffffu, bv, 31 - lane);
+        bi = __shfl_sync(0xffffffffu, bi, 31 - lane);
+        if (better(bv, bi, lv, li)) {
+            const float v = lv;
+            const int i = li;
+            lv = bv, li = bi, bv = v, bi = i;
+        }
+        drop(bv, bi, c);
+#pragma unroll
+        for (int m = 16; m >= 1; m >>= 1) {
+            const float ov = __shfl_xor_sync(0xffffffffu, lv, m);
+            const int oi = __shfl_xor_sync(0xffffffffu, li, m);
+            if (better(ov, oi, lv, li) == ((lane & m) == 0)) lv = ov, li = oi;
+        }
+        if (lane >= kp) {
+            drop(lv, li, c);
+            lv = -INFINITY;
+            li = kNone;
+        }
+    }
+};
+
+struct Part {                                // one chunk of a row
+    float v[kLogprobsMaxTop];
+    int i[kLogprobsMaxTop];
+    float S, U;                              // against v[0]
+};
+
+template <bool BF16>
+struct Raw {
+    uint4 q[BF16 ? 2 : 4];
+};
+
+// Logits [j, j + 16 of every lane) of a row as vectors; j counts from the last 16-byte boundary at
+// or before the row, `mis` elements before its first one. Vectors that reach outside the row are
+// put together from single loads (-inf outside).
+template <bool BF16>
+__device__ __forceinline__ Raw<BF16> load(const uint8_t *base, int j, int mis, int end) {
+    constexpr int E = BF16 ? 8 : 4, N = BF16 ? 2 : 4, SZ = BF16 ? 2 : 4;
+    const int lane = threadIdx.x & 31;
+    Raw<BF16> r;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const int at = j + (n * 32 + lane) * E;
+        if (at >= mis && at + E <= end) {
+            r.q[n] = *reinterpret_cast<const uint4 *>(base + (long long)at * SZ);
+        } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                w[k] = BF16 ? 0xff80ff80u : 0xff800000u;
+                if constexpr (BF16) {
+                    const int e = at + 2 * k;
+                    const uint16_t *p = reinterpret_cast<const uint16_t *>(base) + e;
+                    if (e >= mis && e < end) w[k] = (w[k] & 0xffff0000u) | p[0];
+                    if (e + 1 >= mis && e + 1 < end) w[k] = (w[k] & 0xffffu) | ((uint32_t)p[1] << 16);
+                } else {
+                    const int e = at + k;
+                    if (e >= mis && e < end) w[k] = *(reinterpret_cast<const uint32_t *>(base) + e);
+                }
+            }
+            r.q[n] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+    return r;
+}
+
+// CTA (chunk, row). Bound: the logits, read once; per logit one conversion (16-bit), a running
+// maximum, half of three packed F32 operations, two single ones and the exponential.
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const __grid_constant__ LogprobsArgs a,
+                                                                  int chunk, int n_chunks, float c) {
+    DF_TRACE_KERNEL(TK_LOGPROBS);
+    constexpr int SZ = BF16 ? 2 : 4, E = 16 / SZ;
+    __shared__ float slv[kWarps][32];
+    __shared__ int sli[kWarps][32];
+    __shared__ float top[kWarps];
+    __shared__ float2 sums[kWarps];
+    __shared__ int tau_bits, last;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int r = blockIdx.y + gridDim.y * blockIdx.z, ck = blockIdx.x;
+    if (r >= a.R) return;
+    const int kp = max(a.top_k, 1);
+    const uint8_t *row = static_cast<const uint8_t *>(a.logits) + (size_t)r * a.ld * SZ;
+    const int mis = (int)(reinterpret_cast<uintptr_t>(row) & 15) / SZ;
+    const uint8_t *base = row - mis * SZ;
+    const int begin = ck * chunk, end = min(a.V + mis, begin + chunk);
+    auto ordered = [](float f) {             // order of floats as integers
+        const int b = __float_as_int(f);
+        return b < 0 ? b ^ 0x7fffffff : b;
+    };
+    if (threadIdx.x == 0) tau_bits = ordered(-INFINITY);
+    pdl_trigger();
+    pdl_wait();
+    __syncthreads();
+
+    State st;
+    st.lv = -INFINITY;
+    st.li = kNone;
+    st.mu = -INFINITY;
+    st.S = st.U = 0.f;
+    float2 S2 = make_float2(0.f, 0.f), U2 = make_float2(0.f, 0.f);
+    float tau = -INFINITY;                   // the list's last value, once it is full
+    const int j0 = begin + warp * kStep;
+    Raw<BF16> next;
+    if (j0 < end) next = load<BF16>(base, j0, mis, end);
+    for (int j = j0; j < end; j += kWarps * kStep) {
+        float x[kPerLane];
+#pragma unroll
+        for (int n = 0; n < (BF16 ? 2 : 4); ++n) {
+            const uint32_t w[4] = {next.q[n].x, next.q[n].y, next.q[n].z, next.q[n].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if constexpr (BF16) {
+                    x[n * 8 + 2 * k] = __uint_as_float(w[k] << 16);
+                    x[n * 8 + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+                } else {
+                    x[n * 4 + k] = __uint_as_float(w[k]);
+                }
+            }
+        }
+        if (j + kWarps * kStep < end) next = load<BF16>(base, j + kWarps * kStep, mis, end);
+        float bm = x[0];
+#pragma unroll
+        for (int k = 1; k < kPerLane; ++k) bm = fmaxf(bm, x[k]);
+        const bool first = j == j0;
+        float tau0 = -INFINITY;
+        if (first) {
+            // The kp-th largest of the lanes' maxima: at least kp entries are that large.
+            int rank = 0;
+#pragma unroll 8
+            for (int k = 0; k < 32; ++k) {
+                const float o = __shfl_sync(0xffffffffu, bm, k);
+                rank += o > bm || (o == bm && k < lane);
+            }
+            const unsigned who = __ballot_sync(0xffffffffu, rank == kp - 1);
+            tau0 = who ? __shfl_sync(0xffffffffu, bm, __ffs(who) - 1) : -INFINITY;
+        }
+        const int tb = *reinterpret_cast<volatile int *>(&tau_bits);
+        const float tau_all = __int_as_float(tb < 0 ? tb ^ 0x7fffffff : tb);
+        // Later entries have higher indices than the list's own, so they have to be larger than
+        // its last; another warp's bound may be met by an equal entry of lower index.
+        // And the reference follows the maximum when the exponents could overflow.
+        const bool want = first ? bm >= tau0 : (bm > tau && bm >= tau_all) || (bm - st.mu) * c > 60.f;
+        if (__any_sync(0xffffffffu, want)) {
+            bool changed = false;
+            const float m = warp_max(bm);
+            if (st.mu == -INFINITY) {
+                st.mu = m;
+            } else if ((m - st.mu) * c > 60.f) {
+                st.S += S2.x + S2.y;
+                st.U += U2.x + U2.y;
+                S2 = U2 = make_float2(0.f, 0.f);
+                st.rebase(m, c);
+            }
+#pragma unroll
+            for (int k = 0; k < kPerLane; ++k) {
+                const int idx = j + ((k / E) * 32 + lane) * E + k % E - mis;
+                const bool in = idx >= 0 && idx < end - mis;
+                unsigned bal = __ballot_sync(0xffffffffu, in && (first ? x[k] >= tau0 : (x[k] > tau && x[k] >= tau_all)));
+                while (bal) {
+                    const int src = __ffs(bal) - 1;
+                    bal &= bal - 1;
+                    const float v = __shfl_sync(0xffffffffu, x[k], src);
+                    if (st.insert(v, __shfl_sync(0xffffffffu, idx, src), kp, c)) {
+                        changed = true;
+                        if (lane == src) x[k] = -INFINITY;
+                    }
+                }
+            }
+            if (changed) {
+                tau = __shfl_sync(0xffffffffu, st.lv, kp - 1);
+                const bool full = __shfl_sync(0xffffffffu, st.li, kp - 1) != kNone;
+                if (!full) tau = -INFINITY;
+                if (full && lane == 0) atomicMax(&tau_bits, ordered(tau));
+            }
+        }
+        const float ref = st.mu == -INFINITY ? 0.f : st.mu;
+        const float2 nm = make_float2(-ref, -ref), c2 = make_float2(c, c);
+#pragma unroll
+        for (int k = 0; k < kPerLane; k += 2) {
+            float2 t = mul2(add2(make_float2(x[k], x[k + 1]), nm), c2);
+            t.x = max_nan(t.x, kFloor);
+            t.y = max_nan(t.y, kFloor);
+            const float2 e = make_float2(ex2(t.x), ex2(t.y));
+            S2 = add2(S2, e);
+            U2 = fma2(e, t, U2);
+        }
+    }
+    st.S += S2.x + S2.y;
+    st.U += U2.x + U2.y;
+
+    // Joins the warps' states (all with one reference) in warp 0, in a fixed order.
+    auto join = [&](State &s) {
+        s.S = warp_sum(s.S);
+        s.U = warp_sum(s.U);
+        if (lane != 0) s.S = s.U = 0.f;
+        for (int half = kWarps / 2; half >= 1; half >>= 1) {
+            __syncthreads();
+            if (warp >= half && warp < 2 * half) {
+                slv[warp][lane] = s.lv;
+                sli[warp][lane] = s.li;
+                const float2 v = make_float2(warp_sum(s.S), warp_sum(s.U));
+                if (lane == 0) sums[warp] = v;
+            }
+            __syncthreads();
+            if (warp < half) {
+                s.merge(slv[warp + half][lane], sli[warp + half][lane], kp, c);
+                if (lane == 0) {
+                    s.S += sums[warp + half].x;
+                    s.U += sums[warp + half].y;
+                }
+            }
+        }
+        s.S = warp_sum(s.S);
+        s.U = warp_sum(s.U);
+    };
+    if (lane == 0) top[warp] = st.lv;
+    __syncthreads();
+    float M = top[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) M = fmaxf(M, top[w]);
+    st.rebase(M, c);
+    join(st);
+
+    if (n_chunks > 1) {
+        Part *parts = static_cast<Part *>(a.part) + (size_t)r * n_chunks;
+        if (warp == 0) {
+            parts[ck].v[lane] = st.lv;
+            parts[ck].i[lane] = st.li;
+            if (lane == 0) {
+                parts[ck].S = st.S;
+                parts[ck].U = st.U;
+            }
+            __threadfence();
+            __syncwarp();
+            if (lane == 0) last = atomicAdd(a.counters + r, 1) == n_chunks - 1;
+        }
+        __syncthreads();
+        if (!last) return;
+        __threadfence();
+        if (threadIdx.x == 0) a.counters[r] = 0;
+        M = -INFINITY;
+        for (int k = lane; k < n_chunks; k += 32) M = fmaxf(M, __ldcg(&parts[k].v[0]));
+        M = warp_max(M);
+        st.lv = -INFINITY;
+        st.li = kNone;
+        st.mu = M;
+        st.S = st.U = 0.f;
+        for (int k = warp; k < n_chunks; k += kWarps) {
+            State o;
+            o.mu = __ldcg(&parts[k].v[0]);
+            o.S = __ldcg(&parts[k].S);
+            o.U = __ldcg(&parts[k].U);
+            const float v = __ldcg(&parts[k].v[lane]);
+            const int i = __ldcg(&parts[k].i[lane]);
+            o.rebase(M, c);
+            if (lane == 0) {
+                st.S += o.S;
+                st.U += o.U;
+            }
+            st.merge(v, i, kp, c);
+        }
+        join(st);
+    }
+    if (warp != 0) return;
+
+    // The listed entries but the first complete the sums.
+    const float t = lane > 0 && st.li != kNone ? max_nan((st.lv - M) * c, kFloor) : kFloor;
+    const float e = ex2(t);
+    const float S = st.S + warp_sum(e), Ut = st.U + warp_sum(e * t);
+    const float ls = log1pf(S);
+    const bool bad = !(S <= 3.4028234e38f) || !(fabsf(M) <= 3.4028234e38f);
+    const float nan = __int_as_float(0x7fc00000);
+    if (lane < a.top_k) {
+        a.top_ids[(size_t)r * a.top_k + lane] = st.li;
+        a.top_lp[(size_t)r * a.top_k + lane] = bad ? nan : (st.lv - M) / a.T - ls;
+    }
+    if (lane == 0) {
+        const int tk = a.tokens[r];
+        float lp = 0.f;
+        bool err = bad;
+        if (tk >= 0 && tk < a.V) {
+            const float x = BF16 ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(row)[tk] << 16)
+                                 : reinterpret_cast<const float *>(row)[tk];
+            lp = (x - M) / a.T - ls;
+        } else if (tk != -1) {
+            lp = nan;
+            err = true;
+        }
+        a.logprob[r] = bad ? nan : lp;
+        if (a.entropy) a.entropy[r] = bad ? nan : ls - Ut * 0.69314718f / (1.f + S);
+        if (err) set_status(a.status, DF_EINVAL);
+    }
+}
+
+struct Plan {
+    int chunk, n;
+};
+// A chunk is whole steps of the CTA: as many chunks as give about four CTAs a place on the GPU
+// (so the last wave is short), none below one step.
+Plan plan_of(int R, int V) {
+    const long long step = (long long)kWarps * kStep;
+    const long long target = 16LL * sm_count();
+    long long chunk = ((long long)R * V + target - 1) / target;
+    chunk = (chunk + step - 1) / step * step;
+    if (R > kOpsCounters || chunk > V + 7LL) chunk = (V + 7LL + step - 1) / step * step;
+    Plan p;
+    p.chunk = (int)chunk;
+    p.n = (int)((V + 7LL + chunk - 1) / chunk);
+    return p;
+}
+
+}  // namespace
+
+size_t logprobs_part_bytes(int R, int V) {
+    const Plan p = plan_of(R, V);
+    return p.n > 1 ? (size_t)R * p.n * sizeof(Part) : 0;
+}
+
+int launch_token_logprobs(const LogprobsArgs &a, cudaStream_t s) {
+    const Plan p = plan_of(a.R, a.V);
+    const float c = (float)(1.4426950408889634074 / (double)a.T);
+    const unsigned ry = a.R < 32768 ? (unsigned)a.R : 32768u;
+    const dim3 grid((unsigned)p.n, ry, ((unsigned)a.R + ry - 1) / ry);
+    return a.bf16 ? launch_k("token_logprobs_kernel", token_logprobs_kernel<true>, grid, dim3(kThreads), 0, s,
+                             a, p.chunk, p.n, c)
+                  : launch_k("token_logprobs_kernel", token_logprobs_kernel<false>, grid, dim3(kThreads), 0, s,
+                             a, p.chunk, p.n, c);
+}
+
+}  // namespace df

@@ -1,0 +1,181 @@
+"""GPU parity of the token log probabilities against float64 (oracle/paged.py). A row's log
+probabilities are (x - M) / T - log1p(S): the difference and the quotient are one rounding each
+(2^-24 relative, 2^-22 allowed); a term of S is off by its exponent's three roundings (at most
+3 * 2^-24 * 40 where it still counts) and the exponential's 2^-22, which stays below 2^-17 of S,
+as does the sum (some hundred additions a lane); so the absolute error is below 2^-17 on S / (1 + S)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged as op
+from speculative_decoding_drafter_dflash_gb300 import binding as B
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from speculative_decoding_drafter_dflash_gb300 import build
+    build.build()
+    B.lib()
+
+
+def _run(x, tokens, top, T=1.0, status=None, ws=None, entropy=True):
+    R, V = x.shape
+    f = dict(device=DEV)
+    lp, en = torch.full((R,), 9.0, **f), torch.full((R,), 9.0, **f)
+    ids = torch.full((R, top), -5, dtype=torch.int32, **f) if top else None
+    tl = torch.full((R, top), 9.0, **f) if top else None
+    ws = B.alloc_workspace(B.token_logprobs_workspace_bytes(R, V, top)) if ws is None else ws
+    B.token_logprobs(x, torch.tensor(tokens, dtype=torch.int32, device=DEV), lp, en if entropy else None, ids, tl,
+                     ws, temperature=T, d_status=status)
+    torch.cuda.synchronize()
+    return lp, en, ids, tl
+
+
+def _check(x, tokens, top, T=1.0, out=None):
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    lp, en, ids, tl = out or _run(x, tokens, top, T, st)
+    assert int(st) == 0
+    for r in range(x.shape[0]):
+        a, h, i, t = op.logprobs(x[r].double().cpu().numpy(), T, tokens[r], top)
+        share = -math.expm1(-h) if h < 1 else 1.0            # S / (1 + S) <= 1 - e^-h, roughly
+        tol = 2.0 ** -17 * max(share, 1e-30) + 2.0 ** -22 * abs(a)
+        assert (a == -np.inf and float(lp[r]) == -np.inf) or abs(float(lp[r]) - a) <= tol, (r, float(lp[r]), a)
+        assert abs(float(en[r]) - h) <= 2.0 ** -16 * max(h, 1e-30), (r, float(en[r]), h)
+        if top:
+            assert ids[r].tolist() == i.tolist(), (r, ids[r].tolist(), i.tolist())
+            g = tl[r].double().cpu().numpy()
+            fin = np.isfinite(t)
+            assert np.array_equal(np.isfinite(g), fin)
+            assert np.all(np.abs(g[fin] - t[fin]) <= 2.0 ** -17 + 2.0 ** -22 * np.abs(t[fin]))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("R,V,top,T,pad,shift", [
+    (1, 1, 1, 1.0, 0, 0), (1, 2, 2, 1.0, 0, 0), (3, 31, 31, 0.7, 2, 1), (2, 33, 32, 1.0, 0, 0), (5, 511, 0, 2.0, 1, 3),
+    (4, 4096, 20, 1.0, 0, 0), (3, 4099, 7, 1.3, 13, 5), (2, 50001, 32, 0.5, 0, 0), (1, 248320, 5, 1.0, 0, 0),
+    (16, 262144, 8, 0.7, 0, 0), (700, 1000, 3, 1.0, 1, 0), (2500, 4500, 2, 1.0, 0, 0),
+])
+def test_against_float64(R, V, top, T, pad, shift, dtype):
+    g = torch.Generator(device=DEV).manual_seed(R + V)
+    buf = (3 * torch.randn(R * (V + pad) + shift, generator=g, device=DEV)).to(dtype)
+    x = buf[shift:].view(R, V + pad)[:, :V]
+    tokens = torch.randint(0, V, (R,), generator=g, device=DEV).tolist()
+    if R > 20:
+        out = _run(x, tokens, top, T)
+        pick = [0, 1, R // 2, R - 1]
+        _check(x[pick], [tokens[r] for r in pick], top, T, [None if o is None else o[pick] for o in out])
+    else:
+        _check(x, tokens, top, T)
+
+
+def test_ties_go_to_the_lowest_index():
+    V = 9001
+    x = torch.zeros((4, V), device=DEV)
+    x[1, 5::7] = 1.0
+    x[2] = -math.inf
+    x[2, [8000, 3, 4500, 8999]] = 2.0
+    x[3] = torch.arange(V, device=DEV) // 2500           # every group of equals larger than the list
+    _check(x, [0, 5, 3, 9000], 20)
+    _check(x.to(torch.bfloat16), [0, 5, 3, 9000], 20)
+    _check(-x[[0, 1, 3]], [0, 5, 0], 32)
+
+
+def test_masked_rows_and_few_left():
+    V = 20000
+    g = torch.Generator(device=DEV).manual_seed(5)
+    x = torch.randn((4, V), generator=g, device=DEV)
+    x[0, :19000] = -math.inf                              # the first steps hold nothing
+    x[1, 3:] = -math.inf
+    x[2, :] = -math.inf
+    x[2, 12345] = -400.0                                  # one entry, far from 0
+    x[3, ::2] = torch.finfo(torch.float32).min            # masked by the type's lowest value
+    _check(x, [19500, 1, 12345, 7], 6)
+    _check(x, [5, 5, 5, 5], 0)                            # (masked tokens: -inf)
+
+
+def test_rows_that_rise_or_fall_by_more_than_the_exponent_range():
+    V = 30000
+    up = torch.linspace(-3000, 500, V, device=DEV)
+    x = torch.stack((up, up.flip(0), up * 0 + 1e30, torch.where(torch.arange(V, device=DEV) == 7000, 1e4, up)))
+    _check(x, [V - 1, 0, 5, 7000], 5)
+    _check(x, [V - 2, 1, 9, 6999], 3, 0.1)
+
+
+def test_a_near_certain_row_keeps_its_relative_accuracy():
+    V = 32000
+    x = torch.zeros((2, V), device=DEV)
+    x[0, 777], x[1, 31999] = 25.0, 40.0
+    lp, en, _, _ = _run(x, [777, 31999], 0)
+    for r, m in ((0, 25.0), (1, 40.0)):
+        s = (V - 1) * math.exp(-m)
+        assert abs(float(lp[r]) / -math.log1p(s) - 1) < 1e-5
+        assert abs(float(en[r]) / (math.log1p(s) + s * m / (1 + s)) - 1) < 1e-5
+
+
+def test_tokens_outside_and_rows_without_a_distribution():
+    x = torch.randn((6, 5000), device=DEV)
+    x[1] = -math.inf
+    x[2, 4000] = math.nan
+    x[3, 17] = math.inf
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    lp, en, ids, tl = _run(x, [-1, 0, 0, 17, 4, 8], 4, 1.0, st)
+    assert int(st) == B.DF_EINVAL
+    assert float(lp[0]) == 0.0
+    for r in (1, 2, 3):
+        assert math.isnan(float(lp[r])) and math.isnan(float(en[r])) and bool(torch.isnan(tl[r]).all())
+    _check(x[[0, 4, 5]], [9, 4, 8], 4)
+    for bad in (-2, 5000):
+        st.zero_()
+        lp, en, _, _ = _run(x[:1], [bad], 0, 1.0, st)
+        assert int(st) == B.DF_EINVAL and math.isnan(float(lp[0])) and math.isfinite(float(en[0]))
+    st.zero_()
+    assert float(_run(x[:1], [-1], 0, 1.0, st, entropy=False)[0][0]) == 0.0 and int(st) == 0
+
+
+def test_repeats_bit_for_bit_on_two_streams_and_in_a_graph():
+    x = torch.randn((3, 100000), device=DEV)
+    tok = torch.tensor([5, 6, 7], dtype=torch.int32, device=DEV)
+    size = B.token_logprobs_workspace_bytes(3, 100000, 4)
+    sets = [(B.alloc_workspace(size), torch.zeros(3, device=DEV), torch.zeros(3, device=DEV),
+             torch.zeros((3, 4), dtype=torch.int32, device=DEV), torch.zeros((3, 4), device=DEV)) for _ in range(3)]
+    torch.cuda.synchronize()
+
+    def go(s, stream=None):
+        B.token_logprobs(x, tok, s[1], s[2], s[3], s[4], s[0], stream=stream)
+
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(4):
+        for k in range(2):
+            go(sets[k], streams[k])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        go(sets[2])
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    for s in sets[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(s[1:], sets[0][1:]))
+    _check(x, [5, 6, 7], 4, 1.0, sets[0][1:])
+
+
+def test_scores_the_drafts_of_a_sampled_block():
+    """The drafts that sample_softmax draws, scored from the same logits inside the wider block."""
+    K, V, T = 6, 4096, 0.8
+    g = torch.Generator(device=DEV).manual_seed(3)
+    logits = 2 * torch.randn((2, K + 1, V), generator=g, device=DEV)
+    q = logits[:, 1:].reshape(-1, V).contiguous()
+    tokens = torch.zeros(2 * K, dtype=torch.int32, device=DEV)
+    u = torch.rand(2 * K, generator=g, device=DEV)
+    B.sample_softmax(q, T, u, tokens, B.alloc_workspace(B.sample_softmax_workspace_bytes(2 * K, V)))
+    _check(q, tokens.tolist(), 5, T)
+    lp = torch.zeros(K, device=DEV)
+    ws = B.alloc_workspace(B.token_logprobs_workspace_bytes(K, V, 0))
+    B.token_logprobs(logits[1, 1:], tokens[K:], lp, ws=ws, temperature=T)
+    assert torch.equal(lp, _run(q[K:], tokens[K:].tolist(), 0, T)[0])

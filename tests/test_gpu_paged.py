@@ -1,0 +1,589 @@
+"""GPU parity of the paged 4-bit KV cache against a plain float64 restatement (oracle/paged.py):
+append (norms, rotary positions, quantisation), gather, attention, and a decode loop of them.
+
+Codes and scales must equal the definition's bit for bit. Tolerances of the floats are bounds
+counted from the roundings that the kernels make (2^-24 is half a step of F32):
+  * q: 20 of them on |a| + |b| of a rotated pair, 32 allowed;
+  * attention: a score is at most 2 d / 16 <= 32 accumulations of a sum of |q_i k_i|, so it is off by
+    dx = 2^-19 sum |q k| / sqrt(d) at most; a weighted mean of v moves by at most 2 dx max|v|; the
+    sums over keys (at most 64 accumulations a warp here, the exponential's 2^-22, the joins) add
+    2^-17 of max|v| each way."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged as op
+from speculative_decoding_drafter_dflash_gb300 import binding as B
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from speculative_decoding_drafter_dflash_gb300 import build
+    build.build()
+    B.lib()
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+class Pool:
+    """A cache whose pages are a shuffled part of the pool, every byte set to a pattern first."""
+
+    def __init__(self, lens, extra, nkv, d, page, seed=0, fill=0xAB, k_scale=1.0, v_scale=1.0):
+        rng = np.random.default_rng(seed)
+        need = [-(-(n + e) // page) for n, e in zip(lens, extra)]
+        pages = sum(need) + 3
+        ids = rng.permutation(pages)[:sum(need)]
+        self.table = np.full((len(lens), max(max(need), 1)), -1, dtype=np.int32)
+        at = 0
+        for b, n in enumerate(need):
+            self.table[b, :n] = ids[at:at + n]
+            at += n
+        self.page, self.nkv, self.d, self.lens = page, nkv, d, list(lens)
+        self.seq_len = _i32(self.lens)
+        self.cache = B.PagedKv.empty(pages, page, nkv, d, torch.tensor(self.table, device=DEV), self.seq_len,
+                                     k_scale, v_scale)
+        for t in self.pools():
+            t.fill_(fill)
+
+    def pools(self):
+        c = self.cache
+        return c.k_codes, c.k_scales, c.v_codes, c.v_scales
+
+    def host(self):
+        return [t.cpu().numpy().copy() for t in self.pools()]
+
+    def put(self, host, b, row, k, v):
+        """Rows k, v [nkv, d] of float64 into host copies of the pools."""
+        p, s = self.table[b, row // self.page], row % self.page
+        for (codes, scales), y, sc in (((host[0], host[1]), k, self.cache.c.k_scale),
+                                       ((host[2], host[3]), v, self.cache.c.v_scale)):
+            c, e = op.quantise(y, sc)
+            codes[p, :, s], scales[p, :, s] = op.pack(c), e
+
+    def rows(self, host, b, n):
+        """k, v [n, nkv, d] of sequence b's first n rows."""
+        r = np.arange(n)
+        p, s = self.table[b, r // self.page], r % self.page
+        return (op.values(op.unpack(host[0][p, :, s]), host[1][p, :, s], self.cache.c.k_scale),
+                op.values(op.unpack(host[2][p, :, s]), host[3][p, :, s], self.cache.c.v_scale))
+
+    def fill_random(self, seed):
+        """N(0, 1) rows up to every length (+ what else the pages hold stays the pattern)."""
+        rng = np.random.default_rng(seed)
+        host = self.host()
+        for b, n in enumerate(self.lens):
+            for r in range(n):
+                self.put(host, b, r, rng.standard_normal((self.nkv, self.d)), rng.standard_normal((self.nkv, self.d)))
+        for t, h in zip(self.pools(), host):
+            t.copy_(torch.tensor(h))
+        return host
+
+
+APPEND = [
+    # lens, n_new, n_max, nq, nkv, d, page, rot, axes, norm
+    ([0], [1], 1, 4, 2, 64, 16, 64, 1, True),
+    ([8191], [1], 1, 24, 4, 256, 64, 64, 1, True),
+    ([5, 0, 31, 16], [3, 5, 0, 1], 5, 16, 8, 128, 16, 128, 1, True),
+    ([7, 33], [9, 2], 9, 6, 2, 128, 32, 32, 3, True),
+    ([1, 2, 3], [4, 4, 4], 4, 3, 3, 64, 128, 16, 2, False),
+    ([100, 0], [17, 33], 33, 0, 1, 256, 256, 256, 4, True),
+    ([15], [50], 50, 8, 1, 128, 16, 0, 1, True),
+    ([0], [700], 700, 8, 4, 64, 64, 48, 3, True),
+]
+
+
+def _append_case(lens, n_new, n_max, nq, nkv, d, page, rot, axes, norm, seed=1, k_scale=1.0, v_scale=1.0, far=0):
+    rng = np.random.default_rng(seed)
+    b = len(lens)
+    pool = Pool(lens, n_new, nkv, d, page, seed, k_scale=k_scale, v_scale=v_scale)
+    x = rng.standard_normal((b, n_max, (nq + 2 * nkv) * d)).astype(np.float32)
+    w = [(1 + 0.1 * rng.standard_normal(d)).astype(np.float32) if norm else None for _ in range(2)]
+    freq = 1e4 ** (-np.arange(rot // 2) / max(rot // 2, 1)) if rot else None
+    pos = rng.integers(0, 1000, (axes, b, n_max)).astype(np.int32) + far if axes > 1 or far else None
+    axis = rng.integers(0, axes, rot // 2).astype(np.uint8) if axes > 1 else None
+    return pool, x, w, freq, pos, axis
+
+
+def _append(pool, x, w, freq, pos, axis, n_new, nq, status=None, eps=1e-6):
+    b, n_max = x.shape[:2]
+    d, nkv = pool.d, pool.nkv
+    t = lambda a: None if a is None else torch.tensor(a, device=DEV)
+    xt = t(x)
+    q, k, v = xt.split((nq * d, nkv * d, nkv * d), dim=2)
+    q_out = torch.full((b, n_max, nq, d), 7.0, device=DEV) if nq else None
+    B.kv_append_paged(pool.cache, q if nq else None, k, v, q_out, n_new=None if n_new is None else _i32(n_new),
+                      q_norm=t(w[0]), k_norm=t(w[1]), eps=eps, inv_freq=t(freq), positions=t(pos), axis=t(axis),
+                      d_status=status)
+    torch.cuda.synchronize()
+    return q_out
+
+
+def _append_ref(pool, x, w, freq, pos, axis, n_new, nq, eps=1e-6):
+    host = pool.host()
+    b, n_max = x.shape[:2]
+    d, nkv = pool.d, pool.nkv
+    q_ref = np.full((b, n_max, nq, d), 7.0)
+    q_tol = np.zeros_like(q_ref)
+    for s in range(b):
+        n = n_max if n_new is None else n_new[s]
+        if n == 0:
+            continue
+        y = x[s, :n].astype(np.float64).reshape(n, nq + 2 * nkv, d)
+        p = None
+        if freq is not None:
+            if pos is None:
+                p = np.repeat((pool.lens[s] + np.arange(n))[:, None], len(freq), 1)
+            else:
+                p = pos[(axis if axis is not None else np.zeros(len(freq), int)).astype(int), s, :n].T
+        q_ref[s, :n] = op.norm_rope(y[:, :nq], w[0], eps, freq, p)
+        m = np.abs(op.norm_rope(y[:, :nq], w[0], eps, None, None))
+        if freq is not None:
+            h = len(freq)
+            m[..., :2 * h] = np.tile(m[..., :h] + m[..., h:2 * h], 2)
+        q_tol[s, :n] = 32 * 2.0 ** -24 * m + 1e-37
+        k = op.norm_rope(y[:, nq:nq + nkv], w[1], eps, freq, p)
+        for i in range(n):
+            pool.put(host, s, pool.lens[s] + i, k[i], y[i, nq + nkv:])
+    return host, q_ref, q_tol
+
+
+def _check_append(pool, args, n_new, nq):
+    want, q_ref, q_tol = _append_ref(pool, *args, n_new, nq)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    q_out = _append(pool, *args, n_new, nq, st)
+    assert int(st) == 0
+    for name, a, b in zip(("k codes", "k scales", "v codes", "v scales"), pool.host(), want):
+        assert np.array_equal(a, b), f"{name}: {np.count_nonzero(a != b)} of {a.size} bytes differ"
+    if nq:
+        got = q_out.cpu().numpy().astype(np.float64)
+        assert np.all(np.abs(got - q_ref) <= q_tol), np.abs(got - q_ref).max()
+
+
+@pytest.mark.parametrize("case", APPEND)
+def test_append_equals_the_definition_and_touches_nothing_else(case):
+    pool, *args = _append_case(*case)
+    _check_append(pool, args, case[1], case[3])
+
+
+def test_append_without_n_new_takes_every_row():
+    pool, *args = _append_case([3, 20], [6, 6], 6, 4, 2, 128, 16, 128, 1, True)
+    _check_append(pool, args, None, 4)
+
+
+def test_append_at_far_positions():
+    pool, *args = _append_case([0, 0], [8, 8], 8, 4, 2, 128, 16, 128, 1, True, far=(1 << 30) + 12345)
+    _check_append(pool, args, [8, 8], 4)
+
+
+@pytest.mark.parametrize("ks,vs", [(0.125, 4.0), (2.0 ** -12, 2.0 ** 20)])
+def test_append_with_scales(ks, vs):
+    pool, *args = _append_case([0], [40], 40, 2, 2, 128, 16, 64, 1, True, k_scale=ks, v_scale=vs)
+    _check_append(pool, args, [40], 2)
+
+
+def test_append_many_rows_bit_exact():
+    # 40 000 rows: some hundred lie within F32 rounding of a boundary and are decided in float64
+    pool, x, w, freq, pos, axis = _append_case([77], [5000], 5000, 1, 8, 128, 128, 128, 1, True)
+    xt = torch.tensor(x, device=DEV)
+    q, k, v = xt.split((128, 1024, 1024), dim=2)
+    B.kv_append_paged(pool.cache, None, k, v, None, k_norm=torch.tensor(w[1], device=DEV),
+                      inv_freq=torch.tensor(freq, device=DEV))
+    got = pool.host()
+    y = x[0].astype(np.float64).reshape(5000, 17, 128)
+    p = np.repeat((77 + np.arange(5000))[:, None], 64, 1)
+    r = 77 + np.arange(5000)
+    pg, sl = pool.table[0, r // 128], r % 128
+    for i, rows in ((0, op.norm_rope(y[:, 1:9], w[1], 1e-6, freq, p)), (2, y[:, 9:])):
+        c, s = op.quantise(rows)
+        assert np.array_equal(got[i + 1][pg, :, sl], s)
+        assert np.array_equal(got[i][pg, :, sl], op.pack(c))
+
+
+def _edge_rows(d):
+    """Rows of exact boundaries, tiny, huge and zero values."""
+    rows = []
+    for s in (1.0, 0.4375, 2.0 ** -9, 448.0):
+        mid = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0]) * s
+        near = np.nextafter(mid.astype(np.float32), np.float32(np.inf))
+        below = np.nextafter(mid.astype(np.float32), np.float32(-np.inf))
+        for m in (mid, near, below):
+            row = np.resize(np.concatenate((m, -m)), d)
+            row[::16] = 6 * s                                     # the block's maximum fixes the scale
+            rows.append(row)
+    smid = (op.E4M3[:-1] + op.E4M3[1:]) / 2 * 6                   # maxima at scale boundaries
+    for lo in range(0, len(smid), d // 16):
+        m = np.resize(smid[lo:lo + d // 16], d // 16).astype(np.float32)
+        for t in (m, np.nextafter(m, np.float32(np.inf)), np.nextafter(m, np.float32(0))):
+            row = np.zeros(d)
+            row[::16] = t
+            row[5::16] = -t / 3
+            rows.append(row)
+    rows += [np.zeros(d), np.full(d, 1e-42), np.full(d, 1e30), np.full(d, -3e38), np.full(d, 6 * 2.0 ** -10),
+             np.where(np.arange(d) % 2, -0.0, 0.0), np.resize([1e-4, 5.0], d)]
+    return np.array(rows, dtype=np.float32)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_append_ties_and_extremes(d):
+    e = _edge_rows(d)
+    n = len(e)
+    pool = Pool([0], [n], 1, d, 16)
+    x = np.concatenate((e, e), -1)[None]
+    _check_append(pool, [x, (None, None), None, None, None], [n], 0)
+
+
+def test_append_norm_of_huge_and_tiny_rows():
+    # sums of squares beyond F32's range are taken in float64
+    rng = np.random.default_rng(3)
+    pool = Pool([0], [6], 1, 128, 16)
+    x = rng.standard_normal((1, 6, 256)).astype(np.float32)
+    x *= np.array([1e25, 1e-25, 1e19, 1e-19, 1.0, 0.0], dtype=np.float32)[None, :, None]
+    w = (None, np.ones(128, dtype=np.float32))
+    args = [x, w, 1e4 ** (-np.arange(64) / 64), None, None]
+    want, _, _ = _append_ref(pool, *args, [6], 0, eps=1e-30)
+    _append(pool, *args, [6], 0, eps=1e-30)
+    for a, b in zip(pool.host(), want):
+        assert np.array_equal(a, b)
+
+
+def test_append_values_that_are_not_finite():
+    pool = Pool([0], [3], 1, 128, 16)
+    x = np.ones((1, 3, 256), dtype=np.float32)
+    x[0, 0, 128 + 3], x[0, 1, 128 + 20], x[0, 2, 5] = np.inf, np.nan, -np.inf
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    _append(pool, x, (None, None), None, None, None, [3], 0, st)
+    assert int(st) == B.DF_EINVAL
+    host = pool.host()
+    k, v = pool.rows(host, 0, 3)
+    # a block of ones has the scale e4m3(1 / 6) = 11 / 64 (the grid's step there is 1 / 64), so its
+    # ones are held as 6 * 11 / 64
+    one = 66 / 64
+    assert v[0, 0, 3] == 6 * 448 and np.all(v[0, 0, 16:] == one)
+    assert v[1, 0, 20] == 0.0 and np.all(np.delete(v[1, 0], 20) == one)
+    assert k[2, 0, 5] == -6 * 448
+
+
+def test_append_bad_pages_lengths_and_counts_reach_the_status_and_nothing_else():
+    for what in ("page", "page high", "capacity", "negative length", "count", "axis"):
+        pool, x, w, freq, pos, axis = _append_case([3, 5], [2, 2], 2, 2, 1, 64, 16, 64, 2, True)
+        n_new, bad = [2, 2], 0
+        if what.startswith("page"):
+            pool.cache.page_table[0, 0] = -2 if what == "page" else 1 << 20
+        elif what == "capacity":
+            pool.cache.seq_len[0] = pool.cache.cap
+        elif what == "negative length":
+            pool.cache.seq_len[0] = -4
+        elif what == "count":
+            n_new = [-1, 2]
+        else:
+            axis[0] = 9
+        before = pool.host()
+        st = torch.zeros(1, dtype=torch.int32, device=DEV)
+        _append(pool, x, w, freq, pos, axis, n_new, 2, st)
+        assert int(st) == {"page": B.DF_EINVAL, "page high": B.DF_EINVAL, "axis": B.DF_EINVAL,
+                           "count": B.DF_ESHAPE}.get(what, B.DF_ECAPACITY), what
+        after = pool.host()
+        p1 = pool.table[1, 0]
+        for a, b in zip(before, after):
+            assert np.any(a[p1, :, 5:7] != b[p1, :, 5:7]), what          # the good sequence was stored
+            if what != "axis":
+                keep = np.ones(len(a), bool)
+                keep[p1] = False
+                assert np.array_equal(a[keep], b[keep]), what
+
+
+@pytest.mark.parametrize("d,page,nkv", [(64, 16, 3), (128, 64, 2), (256, 32, 1)])
+def test_gather_gives_the_values_and_leaves_other_rows(d, page, nkv):
+    pool = Pool([70, 5, 40], [0, 0, 0], nkv, d, page, k_scale=0.5, v_scale=8.0)
+    host = pool.fill_random(4)
+    start, n, n_max = [33, 0, 39], [20, 5, 1], 24
+    out = [torch.full((3, nkv, n_max, d), -9.0, device=DEV) for _ in range(2)]
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    B.kv_gather_paged(pool.cache, _i32(n), *out, start=_i32(start), d_status=st)
+    assert int(st) == 0
+    for b in range(3):
+        for got, ref in zip(out, pool.rows(host, b, start[b] + n[b])):
+            assert np.array_equal(got[b, :, :n[b]].cpu().numpy(), ref[start[b]:].transpose(1, 0, 2))
+            assert bool((got[b, :, n[b]:] == -9.0).all())
+    B.kv_gather_paged(pool.cache, None, *out, start=_i32([1 << 30, 0, 0]), d_status=st)
+    assert int(st) == B.DF_ECAPACITY and bool((out[0][0, :, n[0]:] == -9.0).all())
+
+
+# -------------------------------------------------------------------------------- attention
+def _attend(pool, q, n_new, causal, status=None, ws=None, out=None, stream=None):
+    b, blk, nq, d = q.shape
+    out = torch.full((b, blk, nq, d), 5.0, device=DEV) if out is None else out
+    ws = B.alloc_workspace(B.attention_paged_workspace_bytes(pool.cache, blk, nq)) if ws is None else ws
+    B.attention_paged(pool.cache, q, out, ws, n_new=n_new, causal=causal, d_status=status, stream=stream)
+    return out
+
+
+def _attend_ref(pool, host, q, n_new, causal):
+    """Reference and elementwise tolerance; rows that are not written stay 5."""
+    b, blk, nq, d = q.shape
+    ref, tol = np.full(q.shape, 5.0), np.zeros((b, 1, 1, 1))
+    for s in range(b):
+        rows = blk if n_new is None else n_new[s]
+        total = pool.lens[s] + (0 if n_new is None else rows)
+        k, v = pool.rows(host, s, total)
+        limit = [min(total, pool.lens[s] + i + 1) if causal else total for i in range(rows)]
+        ref[s, :rows] = op.attention(q[s, :rows], k, v, limit)
+        if total and rows:
+            dx = 2.0 ** -19 * np.abs(q[s, :rows]).max() * np.abs(k).sum(-1).max() / np.sqrt(d)
+            tol[s] = 2 * (dx + 2.0 ** -17) * np.abs(v).max()
+    return ref, tol
+
+
+ATTEND = [
+    # lens, n_new (None: all rows over the cached ones), blk, nq, nkv, d, page, causal
+    ([64], [5], 5, 4, 2, 64, 16, False),
+    ([0], [1], 1, 4, 2, 64, 16, True),
+    ([0], None, 2, 2, 1, 128, 16, False),
+    ([1, 15, 16, 17, 31, 32, 33, 0], None, 1, 8, 2, 128, 16, False),
+    ([0, 3, 128, 255], [4, 0, 3, 1], 4, 6, 3, 128, 32, True),
+    ([300], [1], 1, 24, 4, 256, 64, True),
+    ([513, 7], [2, 2], 2, 12, 1, 256, 128, True),
+    ([1000], [16], 16, 16, 8, 128, 64, False),
+    ([2100], [16], 16, 4, 2, 128, 16, True),
+    ([130, 64, 0], [9, 30, 17], 30, 6, 2, 64, 16, True),
+    ([90], [12], 12, 16, 1, 256, 16, True),
+    ([4000], [1], 1, 16, 1, 128, 256, True),
+    ([0, 40], [70, 33], 70, 2, 2, 128, 32, True),
+]
+
+
+@pytest.mark.parametrize("case", ATTEND)
+def test_attention_matches_float64(case):
+    lens, n_new, blk, nq, nkv, d, page, causal = case
+    pool = Pool(lens, n_new or [0] * len(lens), nkv, d, page, seed=2)
+    keep, pool.lens = pool.lens, [n + (0 if n_new is None else n_new[i]) for i, n in enumerate(pool.lens)]
+    host = pool.fill_random(5)
+    pool.lens = keep
+    q = np.random.default_rng(6).standard_normal((len(lens), blk, nq, d)).astype(np.float32)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = _attend(pool, torch.tensor(q, device=DEV), None if n_new is None else _i32(n_new), causal, st)
+    ref, tol = _attend_ref(pool, host, q, n_new, causal)
+    got = out.cpu().numpy().astype(np.float64)
+    assert int(st) == 0
+    assert np.all(np.abs(got - ref) <= tol), (np.abs(got - ref).max(), tol.max())
+
+
+def _small(lens=(40, 20), n_new=(3, 2), nq=4, nkv=2, d=128, page=16, seed=7):
+    pool = Pool(lens, n_new, nkv, d, page, seed)
+    pool.lens = [a + b for a, b in zip(lens, n_new)]
+    host = pool.fill_random(seed)
+    pool.lens = list(lens)
+    q = np.random.default_rng(seed + 1).standard_normal((len(lens), max(n_new), nq, d)).astype(np.float32)
+    return pool, host, q
+
+
+def test_attention_does_not_see_what_lies_behind_the_last_row():
+    pool, host, q = _small()
+    for t in pool.pools():
+        t.fill_(0x7F)                       # NaN scales everywhere ...
+    want = None
+    for fill in (0x7F, 0x00, 0xFF):
+        h = [np.full_like(x, fill) for x in host]
+        for b, n in enumerate((43, 22)):    # ... but in the sequences' own rows
+            for r in range(n):
+                p, s = pool.table[b, r // 16], r % 16
+                for a, o in zip(h, host):
+                    a[p, :, s] = o[p, :, s]
+        for t, a in zip(pool.pools(), h):
+            t.copy_(torch.tensor(a))
+        got = _attend(pool, torch.tensor(q, device=DEV), _i32([3, 2]), True).cpu().numpy()
+        assert np.isfinite(got).all()
+        assert want is None or np.array_equal(got, want)
+        want = got
+
+
+def test_attention_rows_of_q_that_are_not_finite_stay_alone():
+    pool, host, q = _small()
+    ref, tol = _attend_ref(pool, host, q, [3, 2], False)
+    q[0, 1, 2, 7], q[1, 0, 0, 3] = np.nan, np.inf
+    got = _attend(pool, torch.tensor(q, device=DEV), _i32([3, 2]), False).cpu().numpy()
+    bad = np.zeros(q.shape[:3], bool)
+    bad[0, 1, 2] = bad[1, 0, 0] = True
+    assert np.isnan(got[bad]).all()
+    assert np.all((np.abs(got - ref) <= tol)[~bad])
+
+
+@pytest.mark.parametrize("size", [1e-30, 1e-3, 1e4, 1e30])
+def test_attention_of_q_of_any_size(size):
+    # tiny q: a plain mean; huge q: the keys of the largest score alone, however far above F16
+    pool, host, q = _small(seed=9)
+    q = (q * np.float32(size)).astype(np.float32)
+    got = _attend(pool, torch.tensor(q, device=DEV), _i32([3, 2]), False).cpu().numpy()
+    ref, tol = _attend_ref(pool, host, q, [3, 2], False)
+    if size > 1e3:                          # the winner decides: rows whose best two are apart
+        ref = ref.astype(np.float64)
+        tol = 1e-5
+    assert np.all(np.abs(got - ref) <= tol), np.abs(got - ref).max()
+
+
+def test_attention_late_and_early_maxima():
+    # scores that rise by far more than the lazy margin along the keys, and that fall
+    for order in (1, -1):
+        pool = Pool([600], [0], 1, 128, 64)
+        host = pool.host()
+        rng = np.random.default_rng(11)
+        u = rng.standard_normal(128)
+        for r in range(600):
+            at = r if order > 0 else 599 - r
+            pool.put(host, 0, r, (u * at / 60)[None], rng.standard_normal((1, 128)))
+        for t, a in zip(pool.pools(), host):
+            t.copy_(torch.tensor(a))
+        q = np.stack([u * f for f in (0.1, 1.0, -1.0, 5.0)])[None, None].astype(np.float32)
+        got = _attend(pool, torch.tensor(q, device=DEV), None, False).cpu().numpy()
+        ref, tol = _attend_ref(pool, host, q, None, False)
+        assert np.all(np.abs(got - ref) <= tol), np.abs(got - ref).max()
+
+
+def test_attention_bad_tables_and_lengths_reach_the_status():
+    for what in ("page", "length", "negative", "count"):
+        pool, host, q = _small()
+        n_new = [3, 2]
+        if what == "page":
+            pool.cache.page_table[0, 1] = 1 << 24
+        elif what == "length":
+            pool.cache.seq_len[0] = pool.cache.cap
+        elif what == "negative":
+            pool.cache.seq_len[0] = -9
+        else:
+            n_new = [4, 2]
+        st = torch.zeros(1, dtype=torch.int32, device=DEV)
+        got = _attend(pool, torch.tensor(q, device=DEV), _i32(n_new), False, st).cpu().numpy()
+        assert int(st) == {"page": B.DF_EINVAL, "count": B.DF_ESHAPE}.get(what, B.DF_ECAPACITY)
+        ref, tol = _attend_ref(pool, host, q, [3, 2], False)
+        assert np.all(np.abs(got[1] - ref[1]) <= tol[1]), what
+
+
+def test_attention_repeats_bit_for_bit_and_shares_a_workspace_between_sizes():
+    pool, host, q = _small(lens=(3000, 2999), n_new=(4, 4), seed=13)
+    other, ohost, oq = _small(lens=(50,), n_new=(20,), nq=8, nkv=1, d=64, seed=14)
+    need = max(B.attention_paged_workspace_bytes(pool.cache, 4, 4),
+               B.attention_paged_workspace_bytes(other.cache, 20, 8), B.token_logprobs_workspace_bytes(3, 9000, 2))
+    ws = B.alloc_workspace(need)
+    qt, oqt = torch.tensor(q, device=DEV), torch.tensor(oq, device=DEV)
+    x = torch.randn((3, 9000), device=DEV)
+    tok, lp = _i32([1, 2, 3]), torch.zeros(3, device=DEV)
+    first = None
+    for _ in range(3):
+        a = _attend(pool, qt, _i32([4, 4]), True, ws=ws).clone()
+        o = _attend(other, oqt, _i32([20]), True, ws=ws).clone()
+        B.token_logprobs(x, tok, lp, ws=ws)
+        got = (a, o, lp.clone())
+        assert first is None or all(torch.equal(p, r) for p, r in zip(first, got))
+        first = got
+    for p, h, got, qq, n in ((pool, host, first[0], q, [4, 4]), (other, ohost, first[1], oq, [20])):
+        ref, tol = _attend_ref(p, h, qq, n, True)
+        assert np.all(np.abs(got.cpu().numpy() - ref) <= tol)
+    want = torch.log_softmax(x.double(), -1)[torch.arange(3), tok.long()]
+    assert float((first[2] - want).abs().max()) <= 2.0 ** -18 + 2.0 ** -22 * float(want.abs().max())
+
+
+def test_two_streams_and_a_captured_graph():
+    pool, host, q = _small(lens=(700, 650), n_new=(2, 2), seed=15)
+    n = _i32([2, 2])
+    qt = torch.tensor(q, device=DEV)
+    ref, tol = _attend_ref(pool, host, q, [2, 2], True)
+    size = B.attention_paged_workspace_bytes(pool.cache, 2, 4)
+    ws = [B.alloc_workspace(size) for _ in range(3)]
+    outs = [torch.zeros_like(qt) for _ in range(3)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for s, w, o in zip(streams, ws, outs):
+            _attend(pool, qt, n, True, ws=w, out=o, stream=s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _attend(pool, qt, n, True, ws=ws[2], out=outs[2])
+    for _ in range(3):
+        outs[2].zero_()
+        graph.replay()
+    torch.cuda.synchronize()
+    for o in outs:
+        assert np.all(np.abs(o.cpu().numpy() - ref) <= tol)
+
+
+def test_decode_loop():
+    """Blocks appended, attended, advanced and partly rolled back, twelve times over: the cache
+    must hold what the kept rows say, the attention must equal float64 and the contiguous
+    df_attention over the gathered rows."""
+    rng = np.random.default_rng(21)
+    nq, nkv, d, page, blk = 8, 2, 128, 16, 4
+    lens = [0, 37]
+    pool = Pool(lens, [12 * blk, 12 * blk], nkv, d, page, 22)
+    freq = 1e4 ** (-np.arange(32) / 32)
+    kept = pool.host()
+    ws = B.alloc_workspace(B.attention_paged_workspace_bytes(pool.cache, blk, nq))
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    for b in range(2):
+        for r in range(lens[b]):
+            pool.put(kept, b, r, rng.standard_normal((nkv, d)), rng.standard_normal((nkv, d)))
+    for t, a in zip(pool.pools(), kept):
+        t.copy_(torch.tensor(a))
+    for step in range(12):
+        n_new = [int(rng.integers(0, blk + 1)), int(rng.integers(1, blk + 1))]
+        x = rng.standard_normal((2, blk, (nq + 2 * nkv) * d)).astype(np.float32)
+        w = [(1 + 0.1 * rng.standard_normal(d)).astype(np.float32) for _ in range(2)]
+        want, _, _ = _append_ref(pool, x, w, freq, None, None, n_new, nq)
+        q_out = _append(pool, x, w, freq, None, None, n_new, nq, st)
+        got = pool.host()
+        for a, b in zip(got, want):
+            assert np.array_equal(a, b)
+        out = _attend(pool, q_out, _i32(n_new), True, st, ws)
+        ref, tol = _attend_ref(pool, got, q_out.cpu().numpy(), n_new, True)
+        assert np.all(np.abs(out.cpu().numpy() - ref) <= tol)
+        B.kv_advance(pool.seq_len, _i32(n_new), pool.cache.cap, st)
+        back = [int(rng.integers(0, n + 1)) for n in n_new]
+        B.kv_rollback(pool.seq_len, _i32(back), st)
+        pool.lens = [a + n - k for a, n, k in zip(pool.lens, n_new, back)]
+        assert pool.seq_len.tolist() == pool.lens and int(st) == 0
+    n_max = max(pool.lens) + 1
+    k, v = (torch.zeros((2, nkv, n_max, d), device=DEV) for _ in range(2))
+    B.kv_gather_paged(pool.cache, pool.seq_len, k, v, d_status=st)
+    q = torch.randn((2, 1, nq, d), device=DEV)
+    flat = torch.zeros_like(q)
+    B.attention(q, k, v, pool.seq_len, flat, B.alloc_workspace(B.attention_workspace_bytes(2, 1, nq, nkv, d, n_max)))
+    paged = _attend(pool, q, None, False, st)
+    # df_attention's own bound against float64 is 1e-4 of the row's size
+    assert float((flat - paged).abs().max()) <= 2e-4 * float(flat.abs().max()) and int(st) == 0
+
+
+def test_advance_clamps():
+    seq, st = _i32([3, 9, 2]), torch.zeros(1, dtype=torch.int32, device=DEV)
+    B.kv_advance(seq, _i32([2, 0, 1]), 10, st)
+    assert seq.tolist() == [5, 9, 3] and int(st) == 0
+    B.kv_advance(seq, _i32([1, 2, 0]), 10, st)
+    assert seq.tolist() == [6, 10, 3] and int(st) == B.DF_ECAPACITY
+
+
+def test_calls_refuse_tensors_that_do_not_fit():
+    pool, _, q = _small()
+    qt = torch.tensor(q, device=DEV)
+    ws = B.alloc_workspace(B.attention_paged_workspace_bytes(pool.cache, 3, 4))
+    out = torch.zeros_like(qt)
+    for bad in (dict(q=qt[:1]), dict(out=out[:, :2]), dict(n_new=_i32([1])), dict(q=qt.double()),
+                dict(q=qt.transpose(1, 2)), dict(ws=ws.float()), dict(ws=ws[:4096].clone()),
+                dict(n_new=torch.zeros(2, dtype=torch.int64, device=DEV)), dict(causal=True, n_new=None),
+                dict(out=out.cpu())):
+        a = dict(q=qt, out=out, ws=ws, n_new=_i32([1, 1]), causal=False)
+        a.update(bad)
+        with pytest.raises((TypeError, ValueError, B.DFlashError)):
+            B.attention_paged(pool.cache, a.pop("q"), a.pop("out"), a.pop("ws"), **a)
+    k = torch.zeros((2, 3, 256), device=DEV)
+    for bad in (dict(k=k[:, :, ::2]), dict(v=k[:1]), dict(k_norm=torch.zeros(64, device=DEV)),
+                dict(inv_freq=torch.ones(64, device=DEV)), dict(positions=torch.zeros((1, 2, 3), device=DEV)),
+                dict(q=torch.zeros((2, 3, 512), device=DEV))):
+        a = dict(q=None, k=k, v=k)
+        a.update(bad)
+        with pytest.raises((TypeError, ValueError)):
+            B.kv_append_paged(pool.cache, a.pop("q"), a.pop("k"), a.pop("v"), **a)

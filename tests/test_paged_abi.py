@@ -1,0 +1,172 @@
+"""The paged 4-bit cache and the token log probabilities without a GPU: what the entry points
+refuse, before any launch, and the workspace sizes."""
+import ctypes
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def L():
+    from speculative_decoding_drafter_dflash_gb300 import build, binding
+    build.build()
+    return binding
+
+
+# Host memory stands in for device pointers: every call below is refused before it would use one.
+_BUF = ctypes.create_string_buffer(4096)
+PTR = (ctypes.addressof(_BUF) + 255) // 256 * 256
+
+
+def _cache(L, **kw):
+    f = dict(k_codes=PTR, v_codes=PTR, k_scales=PTR, v_scales=PTR, page_table=PTR, seq_len=PTR,
+             n_pages=8, page_size=16, max_pages=4, batch=2, n_kv_heads=2, head_dim=128,
+             k_scale=1.0, v_scale=1.0)
+    f.update(kw)
+    return L.PagedKvC(*[f[n] for n, _ in L.PagedKvC._fields_])
+
+
+BAD_CACHES = [
+    (dict(head_dim=96), "DF_ESHAPE", "head_dim"), (dict(head_dim=32), "DF_ESHAPE", "head_dim"),
+    (dict(page_size=8), "DF_ESHAPE", "page_size"), (dict(page_size=48), "DF_ESHAPE", "page_size"),
+    (dict(page_size=512), "DF_ESHAPE", "page_size"), (dict(n_pages=0), "DF_ESHAPE", "n_pages"),
+    (dict(max_pages=0), "DF_ESHAPE", "max_pages"), (dict(batch=0), "DF_ESHAPE", "batch"),
+    (dict(batch=4097), "DF_ESHAPE", "batch"), (dict(n_kv_heads=0), "DF_ESHAPE", "n_kv_heads"),
+    (dict(max_pages=1 << 27), "DF_ESHAPE", "max_pages"),
+    (dict(k_scale=0.75), "DF_EINVAL", "powers of two"), (dict(v_scale=0.0), "DF_EINVAL", "powers of two"),
+    (dict(v_scale=float("nan")), "DF_EINVAL", "powers of two"),
+    (dict(k_scale=float("inf")), "DF_EINVAL", "powers of two"),
+    (dict(k_codes=None), "DF_EINVAL", "k_codes"), (dict(v_codes=PTR + 8), "DF_EINVAL", "v_codes"),
+    (dict(k_scales=None), "DF_EINVAL", "k_scales"), (dict(v_scales=PTR + 4), "DF_EINVAL", "v_scales"),
+    (dict(page_table=None), "DF_EINVAL", "page_table"), (dict(seq_len=PTR + 2), "DF_EINVAL", "seq_len"),
+]
+
+
+def _append(L, c, **kw):
+    f = dict(q=PTR, ldq=512, nq=4, k=PTR, ldk=256, v=PTR, ldv=256, q_norm=None, k_norm=None, eps=1e-6,
+             rope=None, n_new=None, n_max=3, q_out=PTR)
+    f.update(kw)
+    return L.lib().df_kv_append_paged(ctypes.byref(c) if c else None, *f.values(), None, None)
+
+
+def _attend(L, c, **kw):
+    f = dict(q=PTR, n_new=PTR, blk=3, nq=4, causal=0, out=PTR, ws=PTR, ws_bytes=1 << 40)
+    f.update(kw)
+    return L.lib().df_attention_paged(ctypes.byref(c) if c else None, *f.values(), None, None)
+
+
+def _refused(L, rc, code, text):
+    assert L.STATUS_NAMES[rc] == code, (rc, L.last_error())
+    assert text in L.last_error(), L.last_error()
+
+
+@pytest.mark.parametrize("bad,code,text", BAD_CACHES)
+def test_every_call_refuses_a_bad_cache(L, bad, code, text):
+    c = _cache(L, **bad)
+    _refused(L, _append(L, c), code, text)
+    _refused(L, _attend(L, c), code, text)
+    _refused(L, L.lib().df_kv_gather_paged(ctypes.byref(c), None, None, 3, PTR, PTR, None, None), code, text)
+    if code == "DF_ESHAPE":
+        assert L.lib().df_attention_paged_workspace_bytes(ctypes.byref(c), 3, 4) == 0
+
+
+def test_a_null_cache_is_refused(L):
+    _refused(L, _append(L, None), "DF_EINVAL", "cache")
+    _refused(L, _attend(L, None), "DF_EINVAL", "cache")
+    assert L.lib().df_attention_paged_workspace_bytes(None, 3, 4) == 0
+
+
+@pytest.mark.parametrize("kw,code,text", [
+    (dict(n_max=0), "DF_ESHAPE", "n_max"), (dict(nq=0), "DF_EINVAL", "go together"),
+    (dict(q=None), "DF_EINVAL", "go together"), (dict(q_out=None), "DF_EINVAL", "go together"),
+    (dict(q=PTR + 4), "DF_EINVAL", "q is not"), (dict(q_out=PTR + 8), "DF_EINVAL", "q_out"),
+    (dict(ldq=510), "DF_ESHAPE", "ldq"), (dict(ldq=508), "DF_ESHAPE", "ldq"),
+    (dict(k=None), "DF_EINVAL", "k is NULL"), (dict(v=PTR + 4), "DF_EINVAL", "v is not"),
+    (dict(ldk=252), "DF_ESHAPE", "ldk"), (dict(ldv=258), "DF_ESHAPE", "ldv"),
+    (dict(eps=-1.0), "DF_EINVAL", "eps"), (dict(eps=float("nan")), "DF_EINVAL", "eps"),
+    (dict(k_norm=PTR + 1), "DF_EINVAL", "k_norm"),
+])
+def test_append_refusals(L, kw, code, text):
+    _refused(L, _append(L, _cache(L), **kw), code, text)
+
+
+@pytest.mark.parametrize("rope,code,text", [
+    ((None, None, None, 64, 1), "DF_EINVAL", "inv_freq"), ((PTR, None, None, 24, 1), "DF_ESHAPE", "rotary_dim"),
+    ((PTR, None, None, 144, 1), "DF_ESHAPE", "rotary_dim"), ((PTR, None, None, 0, 1), "DF_ESHAPE", "rotary_dim"),
+    ((PTR, None, None, 64, 0), "DF_ESHAPE", "n_axes"), ((PTR, None, None, 64, 5), "DF_ESHAPE", "n_axes"),
+    ((PTR + 4, None, None, 64, 1), "DF_EINVAL", "inv_freq"), ((PTR, PTR + 2, None, 64, 1), "DF_EINVAL", "positions"),
+])
+def test_rope_refusals(L, rope, code, text):
+    r = L.RopeC(*rope)
+    _refused(L, _append(L, _cache(L), rope=ctypes.byref(r)), code, text)
+
+
+@pytest.mark.parametrize("kw,code,text", [
+    (dict(blk=0), "DF_ESHAPE", "blk"), (dict(nq=3), "DF_ESHAPE", "nq"), (dict(nq=0), "DF_ESHAPE", "nq"),
+    (dict(q=None), "DF_EINVAL", "q is NULL"), (dict(out=PTR + 8), "DF_EINVAL", "out"),
+    (dict(causal=2), "DF_EINVAL", "causal"), (dict(causal=1, n_new=None), "DF_EINVAL", "needs n_new"),
+    (dict(ws=None), "DF_EWORKSPACE", "workspace"), (dict(ws=PTR + 16), "DF_EWORKSPACE", "256-byte"),
+    (dict(ws_bytes=4096), "DF_EWORKSPACE", "smaller"), (dict(blk=1 << 26), "DF_ESHAPE", "query heads"),
+])
+def test_attention_refusals(L, kw, code, text):
+    _refused(L, _attend(L, _cache(L), **kw), code, text)
+
+
+def test_attention_refuses_more_work_than_it_can_index(L):
+    c = _cache(L, max_pages=1 << 20, page_size=256, batch=4096, n_kv_heads=64)
+    _refused(L, _attend(L, c, nq=64), "DF_ESHAPE", "pieces")
+
+
+@pytest.mark.parametrize("kw,code,text", [
+    (dict(R=0), "DF_ESHAPE", "R=0"), (dict(V=0), "DF_ESHAPE", "V=0"), (dict(bf16=2), "DF_EINVAL", "bf16"),
+    (dict(ld=99), "DF_ESHAPE", "ld"), (dict(T=0.0), "DF_EINVAL", "temperature"),
+    (dict(T=-1.0), "DF_EINVAL", "temperature"), (dict(T=float("nan")), "DF_EINVAL", "temperature"),
+    (dict(T=float("inf")), "DF_EINVAL", "temperature"), (dict(logits=None), "DF_EINVAL", "logits"),
+    (dict(logits=PTR + 2), "DF_EINVAL", "logits"), (dict(logits=PTR + 1, bf16=1), "DF_EINVAL", "logits"),
+    (dict(tokens=None), "DF_EINVAL", "tokens"), (dict(lp=None), "DF_EINVAL", "logprob"),
+    (dict(k=33), "DF_ESHAPE", "top_k"), (dict(k=-1), "DF_ESHAPE", "top_k"), (dict(V=4, ld=4, k=5), "DF_ESHAPE", "top_k"),
+    (dict(ids=None), "DF_EINVAL", "top_ids"), (dict(top=None), "DF_EINVAL", "top_logprobs"),
+    (dict(ws=None), "DF_EWORKSPACE", "workspace"), (dict(ws=PTR + 128), "DF_EWORKSPACE", "256-byte"),
+    (dict(n=64), "DF_EWORKSPACE", "smaller"),
+])
+def test_logprobs_refusals(L, kw, code, text):
+    f = dict(logits=PTR, bf16=0, R=2, V=100, ld=100, T=1.0, tokens=PTR, lp=PTR, ent=None, k=3, ids=PTR,
+             top=PTR, ws=PTR, n=1 << 40)
+    f.update(kw)
+    _refused(L, L.lib().df_token_logprobs(*f.values(), None, None), code, text)
+    if code == "DF_ESHAPE" and "ld" not in kw:
+        assert L.lib().df_token_logprobs_workspace_bytes(f["R"], f["V"], f["k"]) == 0
+
+
+def test_advance_refusals(L):
+    _refused(L, L.lib().kv_advance(PTR, PTR, 0, 8, None, None), "DF_ESHAPE", "B=0")
+    _refused(L, L.lib().kv_advance(PTR, PTR, 1, 0, None, None), "DF_ESHAPE", "cap")
+    _refused(L, L.lib().kv_advance(PTR, None, 1, 8, None, None), "DF_EINVAL", "NULL")
+
+
+def test_workspace_sizes(L):
+    q = L.lib().df_attention_paged_workspace_bytes
+    c = _cache(L)
+    assert 0 < q(ctypes.byref(c), 1, 4) < 1 << 26 and 0 < q(ctypes.byref(c), 8, 4) < 1 << 26
+    # as many rows as asked for, and no more for longer tables: the split is by CTA
+    assert q(ctypes.byref(c), 1, 4) == q(ctypes.byref(_cache(L, max_pages=1 << 16)), 1, 4)
+    w = L.lib().df_token_logprobs_workspace_bytes
+    assert 0 < w(1, 64, 0) <= w(16, 262144, 8) < 1 << 26
+
+
+def test_binding_refuses_what_the_kernels_would_misread(L):
+    f = torch.zeros((2, 3, 256))
+    u = torch.zeros((8, 2, 16, 64), dtype=torch.uint8)
+    s = torch.zeros((8, 2, 16, 8), dtype=torch.uint8)
+    table, n = torch.zeros((2, 4), dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(TypeError, match="^k_codes: expected a contiguous CUDA torch.uint8"):
+        L.PagedKv(u, s, u, s, table, n)
+    with pytest.raises(ValueError, match="do not fit"):
+        L.PagedKv(u, s[:, :, :, :4], u, s, table, n)
+    with pytest.raises(ValueError, match="do not fit"):
+        L.PagedKv(u, s, u, s, table, n[:1])
+    with pytest.raises(TypeError, match="^k: expected a CUDA"):
+        L._rows(f, 2, 3, 256, "k")
+    with pytest.raises(TypeError, match="^logits: expected CUDA"):
+        L.token_logprobs(torch.zeros((2, 8)), n, torch.zeros(2))
+    assert torch.equal(L.rope_frequencies(1e4, 4, "cpu"), torch.tensor([1.0, 1e-2], dtype=torch.float64))
