@@ -83,21 +83,18 @@ struct State {
         }
         mu = m;
     }
-    // Entry (v, i), the same in every lane, if it is among the best kp; the entry it displaces
-    // goes to lane 0's sums. True if it was taken.
-    __device__ bool insert(float v, int i, int kp, float c) {
+    // The best kp of this list and of 32 entries in any order, one a lane.
+    __device__ void take(float v, int i, int kp, float c) {
         const int lane = threadIdx.x & 31;
-        const unsigned ahead = __ballot_sync(0xffffffffu, better(lv, li, v, i));
-        const int pos = __popc(ahead);
-        if (pos >= kp) return false;
-        const float ev = __shfl_sync(0xffffffffu, lv, kp - 1), uv = __shfl_up_sync(0xffffffffu, lv, 1);
-        const int ei = __shfl_sync(0xffffffffu, li, kp - 1), ui = __shfl_up_sync(0xffffffffu, li, 1);
-        if (lane >= pos && lane < kp) {
-            lv = lane == pos ? v : uv;
-            li = lane == pos ? i : ui;
-        }
-        if (lane == 0) drop(ev, ei, c);
-        return true;
+#pragma unroll
+        for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll
+            for (int m = k >> 1; m >= 1; m >>= 1) {
+                const float ov = __shfl_xor_sync(0xffffffffu, v, m);
+                const int oi = __shfl_xor_sync(0xffffffffu, i, m);
+                if (better(ov, oi, v, i) == (((lane & m) == 0) == ((lane & k) == 0))) v = ov, i = oi;
+            }
+        merge(v, i, kp, c);
     }
     // The best kp of this list and of (bv, bi), sorted the same way; the rest goes to the sums.
     __device__ void merge(float bv, int bi, int kp, float c) {
@@ -172,15 +169,19 @@ __device__ __forceinline__ Raw<BF16> load(const uint8_t *base, int j, int mis, i
 // CTA (chunk, row). Bound: the logits, read once; per logit one conversion (16-bit), a running
 // maximum, half of three packed F32 operations, two single ones and the exponential.
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const __grid_constant__ LogprobsArgs a,
+__global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const __grid_constant__ LogprobsArgs a,
                                                                   int chunk, int n_chunks, float c) {
     DF_TRACE_KERNEL(TK_LOGPROBS);
     constexpr int SZ = BF16 ? 2 : 4, E = 16 / SZ;
     __shared__ float slv[kWarps][32];
     __shared__ int sli[kWarps][32];
-    __shared__ float top[kWarps];
+    __shared__ float tau_s, top_s;
+    __shared__ int count[kWarps];
     __shared__ float2 sums[kWarps];
-    __shared__ int tau_bits, last;
+    __shared__ float2 bound[kWarps];
+    __shared__ int last;
+    __shared__ float held_v[kWarps][32 + kStep];   // entries on their way to the warp's list
+    __shared__ int held_i[kWarps][32 + kStep];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int r = blockIdx.y + gridDim.y * blockIdx.z, ck = blockIdx.x;
     if (r >= a.R) return;
@@ -189,30 +190,81 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const __grid_c
     const int mis = (int)(reinterpret_cast<uintptr_t>(row) & 15) / SZ;
     const uint8_t *base = row - mis * SZ;
     const int begin = ck * chunk, end = min(a.V + mis, begin + chunk);
-    auto ordered = [](float f) {             // order of floats as integers
-        const int b = __float_as_int(f);
-        return b < 0 ? b ^ 0x7fffffff : b;
-    };
-    if (threadIdx.x == 0) tau_bits = ordered(-INFINITY);
     pdl_trigger();
     pdl_wait();
-    __syncthreads();
 
-    State st;
+    State st;                                // warp 0's list is the CTA's; the others' are overflow
     st.lv = -INFINITY;
     st.li = kNone;
     st.mu = -INFINITY;
     st.S = st.U = 0.f;
     float2 S2 = make_float2(0.f, 0.f), U2 = make_float2(0.f, 0.f);
-    float tau = -INFINITY;                   // the list's last value, once it is full
-    const int j0 = begin + warp * kStep;
-    Raw<BF16> next;
-    if (j0 < end) next = load<BF16>(base, j0, mis, end);
-    for (int j = j0; j < end; j += kWarps * kStep) {
-        float x[kPerLane];
+    float tau = -INFINITY;                   // entries to list are larger (later indices lose ties)
+    int held = 0;
+    // The reference follows the maximum m of what comes when the exponents could overflow.
+    auto follow = [&](float m) {
+        if (st.mu == -INFINITY) {
+            st.mu = m;
+        } else if ((m - st.mu) * c > 60.f) {
+            st.S += S2.x + S2.y;
+            st.U += U2.x + U2.y;
+            S2 = U2 = make_float2(0.f, 0.f);
+            st.rebase(m, c);
+        }
+    };
+    // The CTA's list takes what the warps hold, in warp order; tau becomes its last value.
+    auto collect = [&]() {
+        if (warp != 0) {
+            slv[warp][lane] = st.lv;
+            sli[warp][lane] = st.li;
+            st.lv = -INFINITY;
+            st.li = kNone;
+        }
+        if (lane == 0) count[warp] = held;
+        held = 0;
+        __syncthreads();
+        if (warp == 0) {
+            int first[kWarps + 1];
+            first[0] = 0;
+            float m = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                first[w + 1] = first[w] + count[w];
+                if (w > 0) m = fmaxf(m, slv[w][0]);
+            }
+            for (int at = lane; at < first[kWarps]; at += 32) {
+                int w = 0;
+#pragma unroll
+                for (int k = 1; k < kWarps; ++k) w += at >= first[k];
+                int from = 0;
+#pragma unroll
+                for (int k = 1; k < kWarps; ++k) from = w == k ? first[k] : from;
+                m = fmaxf(m, held_v[w][at - from]);
+            }
+            follow(warp_max(m));
+            for (int base = 0; base < first[kWarps]; base += 32) {
+                const int at = base + lane;
+                int w = 0, from = 0;
+#pragma unroll
+                for (int k = 1; k < kWarps; ++k) {
+                    w += at >= first[k];
+                    from = at >= first[k] ? first[k] : from;
+                }
+                const bool in = at < first[kWarps];
+                st.take(in ? held_v[w][at - from] : -INFINITY, in ? held_i[w][at - from] : kNone, kp, c);
+            }
+            for (int w = 1; w < kWarps; ++w)
+                if (sli[w][0] != kNone) st.merge(slv[w][lane], sli[w][lane], kp, c);
+            if (lane == kp - 1) tau_s = st.li == kNone ? -INFINITY : st.lv;
+            if (lane == 0) top_s = st.lv;
+        }
+        __syncthreads();
+        tau = tau_s;
+    };
+    auto unpack = [](const Raw<BF16> &q, float (&x)[kPerLane]) {
 #pragma unroll
         for (int n = 0; n < (BF16 ? 2 : 4); ++n) {
-            const uint32_t w[4] = {next.q[n].x, next.q[n].y, next.q[n].z, next.q[n].w};
+            const uint32_t w[4] = {q.q[n].x, q.q[n].y, q.q[n].z, q.q[n].w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 if constexpr (BF16) {
@@ -223,81 +275,151 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const __grid_c
                 }
             }
         }
-        if (j + kWarps * kStep < end) next = load<BF16>(base, j + kWarps * kStep, mis, end);
-        float bm = x[0];
+    };
+    auto largest = [](const float (&x)[kPerLane]) {
+        float m = x[0];
 #pragma unroll
-        for (int k = 1; k < kPerLane; ++k) bm = fmaxf(bm, x[k]);
-        const bool first = j == j0;
-        float tau0 = -INFINITY;
-        if (first) {
-            // The kp-th largest of the lanes' maxima: at least kp entries are that large.
-            int rank = 0;
-#pragma unroll 8
-            for (int k = 0; k < 32; ++k) {
-                const float o = __shfl_sync(0xffffffffu, bm, k);
-                rank += o > bm || (o == bm && k < lane);
-            }
-            const unsigned who = __ballot_sync(0xffffffffu, rank == kp - 1);
-            tau0 = who ? __shfl_sync(0xffffffffu, bm, __ffs(who) - 1) : -INFINITY;
+        for (int k = 1; k < kPerLane; ++k) m = fmaxf(m, x[k]);
+        return m;
+    };
+    constexpr int kRowsOfStep = kWarps * kStep;
+    const int j0 = begin + warp * kStep;
+    Raw<BF16> next;
+    if (j0 < end) next = load<BF16>(base, j0, mis, end);
+    // The first step's bound of the kp-th largest entry: any warp's kp-th largest lane maximum, or
+    // what the ceil(kp / 8)-th lane maxima of all warps reach. Afterwards the list's last value,
+    // after 1, 3, 9, ... steps. (The same on every run, so the sums' order is too.)
+    float tau0;
+    {
+        const int share = (kp + kWarps - 1) / kWarps - 1;
+        float bm = -INFINITY;
+        if (j0 < end) {
+            float x[kPerLane];
+            unpack(next, x);
+            bm = largest(x);
         }
-        const int tb = *reinterpret_cast<volatile int *>(&tau_bits);
-        const float tau_all = __int_as_float(tb < 0 ? tb ^ 0x7fffffff : tb);
-        // Later entries have higher indices than the list's own, so they have to be larger than
-        // its last; another warp's bound may be met by an equal entry of lower index.
-        // And the reference follows the maximum when the exponents could overflow.
-        const bool want = first ? bm >= tau0 : (bm > tau && bm >= tau_all) || (bm - st.mu) * c > 60.f;
-        if (__any_sync(0xffffffffu, want)) {
-            bool changed = false;
-            const float m = warp_max(bm);
-            if (st.mu == -INFINITY) {
-                st.mu = m;
-            } else if ((m - st.mu) * c > 60.f) {
-                st.S += S2.x + S2.y;
-                st.U += U2.x + U2.y;
-                S2 = U2 = make_float2(0.f, 0.f);
-                st.rebase(m, c);
-            }
+        int rank = 0;
+#pragma unroll 8
+        for (int k = 0; k < 32; ++k) {
+            const float o = __shfl_sync(0xffffffffu, bm, k);
+            rank += o > bm || (o == bm && k < lane);
+        }
+        const unsigned a1 = __ballot_sync(0xffffffffu, rank == kp - 1);
+        const unsigned a2 = __ballot_sync(0xffffffffu, rank == share);
+        const float b1 = __shfl_sync(0xffffffffu, bm, a1 ? __ffs(a1) - 1 : 0);
+        const float b2 = __shfl_sync(0xffffffffu, bm, a2 ? __ffs(a2) - 1 : 0);
+        if (lane == 0) bound[warp] = make_float2(a1 ? b1 : -INFINITY, a2 ? b2 : -INFINITY);
+        __syncthreads();
+        float any = -INFINITY, every = INFINITY;
 #pragma unroll
-            for (int k = 0; k < kPerLane; ++k) {
-                const int idx = j + ((k / E) * 32 + lane) * E + k % E - mis;
-                const bool in = idx >= 0 && idx < end - mis;
-                unsigned bal = __ballot_sync(0xffffffffu, in && (first ? x[k] >= tau0 : (x[k] > tau && x[k] >= tau_all)));
-                while (bal) {
-                    const int src = __ffs(bal) - 1;
-                    bal &= bal - 1;
-                    const float v = __shfl_sync(0xffffffffu, x[k], src);
-                    if (st.insert(v, __shfl_sync(0xffffffffu, idx, src), kp, c)) {
-                        changed = true;
-                        if (lane == src) x[k] = -INFINITY;
+        for (int w = 0; w < kWarps; ++w) {
+            any = fmaxf(any, bound[w].x);
+            every = fminf(every, bound[w].y);
+        }
+        tau0 = fmaxf(any, every);
+    }
+    const int steps = end > begin ? (end - begin + kRowsOfStep - 1) / kRowsOfStep : 0;
+    for (int it = 0, due = 1; it < steps; ++it) {
+        if (it == due) {
+            collect();
+            due *= 3;
+        }
+        const int j = j0 + it * kRowsOfStep;
+        if (j >= end) continue;
+        float x[kPerLane];
+        unpack(next, x);
+        if (j + kRowsOfStep < end) next = load<BF16>(base, j + kRowsOfStep, mis, end);
+        float gm[4];                         // of every four
+#pragma unroll
+        for (int k = 0; k < 4; ++k) gm[k] = fmaxf(fmaxf(x[4 * k], x[4 * k + 1]), fmaxf(x[4 * k + 2], x[4 * k + 3]));
+        const float bm = fmaxf(fmaxf(gm[0], gm[1]), fmaxf(gm[2], gm[3]));
+        const bool want = (it == 0 ? bm >= tau0 : bm > tau) || (bm - st.mu) * c > 60.f;
+        if (__any_sync(0xffffffffu, want)) {
+            follow(warp_max(bm));
+            // What a held entry leaves in the step: nothing in the sums.
+            const float at0 = st.mu == -INFINITY ? 0.f : st.mu, out = at0 - fmaxf(1000.f / c, fabsf(at0));
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              if (!__any_sync(0xffffffffu, it == 0 ? gm[g] >= tau0 : gm[g] > tau)) continue;
+#pragma unroll
+              for (int k = 4 * g; k < 4 * g + 4; ++k) {
+                bool p = it == 0 ? x[k] >= tau0 : x[k] > tau;
+                unsigned bal = __ballot_sync(0xffffffffu, p);
+                if (bal) {
+                    const int idx = j + ((k / E) * 32 + lane) * E + k % E - mis;
+                    if (it == 0 && tau0 == -INFINITY) {      // (places outside the row are -inf too)
+                        p = p && idx >= 0 && idx < end - mis;
+                        bal = __ballot_sync(0xffffffffu, p);
                     }
+                    if (p) {
+                        const int at = held + __popc(bal & ((1u << lane) - 1));
+                        held_v[warp][at] = x[k];
+                        held_i[warp][at] = idx;
+                        x[k] = out;
+                    }
+                    held += __popc(bal);
                 }
+              }
             }
-            if (changed) {
-                tau = __shfl_sync(0xffffffffu, st.lv, kp - 1);
-                const bool full = __shfl_sync(0xffffffffu, st.li, kp - 1) != kNone;
-                if (!full) tau = -INFINITY;
-                if (full && lane == 0) atomicMax(&tau_bits, ordered(tau));
+            // Far more than expected (ties, rising rows): the warp's own list takes them.
+            while (held >= 32) {
+                __syncwarp();
+                held -= 32;
+                st.take(held_v[warp][held + lane], held_i[warp][held + lane], kp, c);
+                __syncwarp();
+                if (__shfl_sync(0xffffffffu, st.li, kp - 1) != kNone)
+                    tau = fmaxf(tau, __shfl_sync(0xffffffffu, st.lv, kp - 1));
             }
         }
         const float ref = st.mu == -INFINITY ? 0.f : st.mu;
         const float2 nm = make_float2(-ref, -ref), c2 = make_float2(c, c);
+        float2 Sn = S2, Un = U2;
 #pragma unroll
         for (int k = 0; k < kPerLane; k += 2) {
-            float2 t = mul2(add2(make_float2(x[k], x[k + 1]), nm), c2);
-            t.x = max_nan(t.x, kFloor);
-            t.y = max_nan(t.y, kFloor);
+            const float2 t = mul2(add2(make_float2(x[k], x[k + 1]), nm), c2);
             const float2 e = make_float2(ex2(t.x), ex2(t.y));
-            S2 = add2(S2, e);
-            U2 = fma2(e, t, U2);
+            Sn = add2(Sn, e);
+            Un = fma2(e, t, Un);
         }
+        // An entry of -inf is 0 times -inf in U: a step that holds one is taken again with the
+        // exponents bounded (which a NaN survives).
+        const float nan = Un.x + Un.y;
+        if (__any_sync(0xffffffffu, nan != nan)) {
+            Sn = S2;
+            Un = U2;
+#pragma unroll
+            for (int k = 0; k < kPerLane; k += 2) {
+                float2 t = mul2(add2(make_float2(x[k], x[k + 1]), nm), c2);
+                t.x = max_nan(t.x, kFloor);
+                t.y = max_nan(t.y, kFloor);
+                const float2 e = make_float2(ex2(t.x), ex2(t.y));
+                Sn = add2(Sn, e);
+                Un = fma2(e, t, Un);
+            }
+        }
+        S2 = Sn;
+        U2 = Un;
     }
+    collect();
     st.S += S2.x + S2.y;
     st.U += U2.x + U2.y;
+    float M = top_s;
+    st.rebase(M, c);
+    st.S = warp_sum(st.S);
+    st.U = warp_sum(st.U);
+    if (lane == 0) sums[warp] = make_float2(st.S, st.U);
+    __syncthreads();
+    if (warp == 0) {
+        st.S = st.U = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            st.S += sums[w].x;
+            st.U += sums[w].y;
+        }
+    }
 
     // Joins the warps' states (all with one reference) in warp 0, in a fixed order.
     auto join = [&](State &s) {
-        s.S = warp_sum(s.S);
-        s.U = warp_sum(s.U);
         if (lane != 0) s.S = s.U = 0.f;
         for (int half = kWarps / 2; half >= 1; half >>= 1) {
             __syncthreads();
@@ -319,13 +441,6 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const __grid_c
         s.S = warp_sum(s.S);
         s.U = warp_sum(s.U);
     };
-    if (lane == 0) top[warp] = st.lv;
-    __syncthreads();
-    float M = top[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) M = fmaxf(M, top[w]);
-    st.rebase(M, c);
-    join(st);
 
     if (n_chunks > 1) {
         Part *parts = static_cast<Part *>(a.part) + (size_t)r * n_chunks;
@@ -351,20 +466,35 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const __grid_c
         st.li = kNone;
         st.mu = M;
         st.S = st.U = 0.f;
-        for (int k = warp; k < n_chunks; k += kWarps) {
-            State o;
-            o.mu = __ldcg(&parts[k].v[0]);
-            o.S = __ldcg(&parts[k].S);
-            o.U = __ldcg(&parts[k].U);
-            const float v = __ldcg(&parts[k].v[lane]);
-            const int i = __ldcg(&parts[k].i[lane]);
-            o.rebase(M, c);
-            if (lane == 0) {
-                st.S += o.S;
-                st.U += o.U;
+        for (int k0 = warp; k0 < n_chunks; k0 += 4 * kWarps) {
+            float v[4], om[4], oS[4], oU[4];
+            int i[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int k = min(k0 + u * kWarps, n_chunks - 1);
+                om[u] = __ldcg(&parts[k].v[0]);
+                oS[u] = __ldcg(&parts[k].S);
+                oU[u] = __ldcg(&parts[k].U);
+                v[u] = __ldcg(&parts[k].v[lane]);
+                i[u] = __ldcg(&parts[k].i[lane]);
             }
-            st.merge(v, i, kp, c);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (k0 + u * kWarps >= n_chunks) break;
+                State o;
+                o.mu = om[u];
+                o.S = oS[u];
+                o.U = oU[u];
+                o.rebase(M, c);
+                if (lane == 0) {
+                    st.S += o.S;
+                    st.U += o.U;
+                }
+                st.merge(v[u], i[u], kp, c);
+            }
         }
+        st.S = warp_sum(st.S);
+        st.U = warp_sum(st.U);
         join(st);
     }
     if (warp != 0) return;
@@ -405,7 +535,7 @@ struct Plan {
 // (so the last wave is short), none below one step.
 Plan plan_of(int R, int V) {
     const long long step = (long long)kWarps * kStep;
-    const long long target = 16LL * sm_count();
+    const long long target = 4LL * sm_count();
     long long chunk = ((long long)R * V + target - 1) / target;
     chunk = (chunk + step - 1) / step * step;
     if (R > kOpsCounters || chunk > V + 7LL) chunk = (V + 7LL + step - 1) / step * step;
