@@ -674,8 +674,8 @@ typedef struct {
  *   n_new      device int32 [batch], each in [0, n_max], or NULL: n_max rows each
  *   q_out      device F32 [batch, n_max, n_q_heads, head_dim] out, 16-byte aligned (NULL with
  *              q): normed and rotated q
- * Row i < n_new[b] is stored as cache row seq_len[b] + i; the others are neither read nor written
- * (in q_out as in the cache). seq_len is not changed: the layers of a step append at the same
+ * Row i < n_new[b] is stored as cache row seq_len[b] + i; the others are not used, and nothing is
+ * written for them (in q_out as in the cache). seq_len is not changed: the layers of a step append at the same
  * rows, then kv_advance moves it. Rows to append must not be shared by two sequences.
  * Device status: DF_ESHAPE (n_new out of range, clamped), DF_ECAPACITY (row past max_pages pages,
  * skipped; a negative seq_len), DF_EINVAL (page id outside [0, n_pages), skipped; an axis

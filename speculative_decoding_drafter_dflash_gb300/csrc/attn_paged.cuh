@@ -1,0 +1,289 @@
+// What the two forms of the paged attention share: the split of the work over the CTAs and the
+// join of partial results.
+//
+// The keys of every (sequence, KV head, block of query rows), a task, form a line of units; the
+// line is cut into equal pieces, one per CTA, so lengths may be as ragged as they like. Few tasks
+// are padded to whole pieces instead, so that a CTA works on one task only. Otherwise every task is
+// followed by EXTRA empty places, for the time that a task costs besides its units (else the CTAs
+// with the short sequences come last). A task that lies in several CTAs leaves partial results
+// (O, m, l), joined in CTA order by the last to arrive.
+#pragma once
+
+#include "paged.cuh"
+
+namespace df {
+
+struct SeqInfo {
+    int len, rows, total;        // rows cached before, query rows, keys
+};
+__device__ __forceinline__ SeqInfo seq_info(const AttnPagedArgs &a, int b, bool report) {
+    SeqInfo s;
+    const long long cap = (long long)a.c.max_pages * a.c.page_size;
+    s.len = a.c.seq_len[b];
+    s.rows = a.n_new ? a.n_new[b] : a.blk;
+    if (s.rows < 0 || s.rows > a.blk) {
+        if (report) set_status(a.status, DF_ESHAPE);
+        s.rows = min(max(s.rows, 0), a.blk);
+    }
+    long long t = (long long)s.len + (a.n_new ? s.rows : 0);
+    if (s.len < 0 || t > cap) {
+        if (report) set_status(a.status, DF_ECAPACITY);
+        t = t < 0 ? 0 : (t > cap ? cap : t);
+    }
+    s.total = (int)t;
+    return s;
+}
+
+// The line: off[b] is where sequence b's tasks start; every task of b takes `len` units of it.
+struct Line {
+    int total, per;
+    bool pad;
+};
+// One CTA's piece of a task: units [x0, x1) of b's KV head h, query rows [r0, r0 + nr).
+struct Piece {
+    int b, h, r0, nr, x0, x1;
+    int keys, len;               // the sequence's keys, and rows cached before
+    int first, last;             // CTAs of the task
+    __device__ bool whole() const { return first == last; }
+};
+
+template <int UNIT>
+__device__ __forceinline__ int units_of(const SeqInfo &s) {
+    return max(1, (s.total + UNIT - 1) / UNIT);
+}
+
+// Places of a task of `units` units.
+template <int EXTRA>
+__device__ __forceinline__ int span_of(const Line &l, int units) {
+    return l.pad ? (units + l.per - 1) / l.per * l.per : units + EXTRA;
+}
+
+// All threads of the CTA; off: shared [batch + 1], misc: shared [64].
+template <int UNIT, int RT, int THREADS, int EXTRA>
+__device__ Line make_line(const AttnPagedArgs &a, int *off, int *misc, int min_per) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = a.c.batch;
+    const int nkv = a.c.n_kv_heads, G = a.nq / nkv, each = (B + THREADS - 1) / THREADS;
+    int units = 0, tasks = 0;
+    SeqInfo mine;
+    for (int k = 0; k < each; ++k) {
+        const int b = tid * each + k;
+        if (b >= B) break;
+        const SeqInfo s = seq_info(a, b, blockIdx.x == 0);
+        mine = s;
+        const int n = nkv * ((s.rows * G + RT - 1) / RT);
+        tasks += n;
+        units += n * units_of<UNIT>(s);
+    }
+    units = __reduce_add_sync(0xffffffffu, units);
+    tasks = __reduce_add_sync(0xffffffffu, tasks);
+    if (lane == 0) {
+        misc[2 * warp] = units;
+        misc[2 * warp + 1] = tasks;
+    }
+    __syncthreads();
+    int U = 0, T = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        U += misc[2 * w];
+        T += misc[2 * w + 1];
+    }
+    __syncthreads();
+    const int grid = (int)gridDim.x;
+    Line l;
+    l.pad = 8 * T <= grid;
+    const int ctas = l.pad ? grid - T : grid;
+    l.per = max(min_per, (U + (l.pad ? 0 : T * EXTRA) + ctas - 1) / ctas);
+    int sum = 0;
+    for (int k = 0; k < each; ++k) {
+        const int b = tid * each + k;
+        if (b >= B) break;
+        const SeqInfo s = each == 1 ? mine : seq_info(a, b, false);
+        sum += nkv * ((s.rows * G + RT - 1) / RT) * span_of<EXTRA>(l, units_of<UNIT>(s));
+    }
+    int inc = sum;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, inc, m);
+        if (lane >= m) inc += o;
+    }
+    if (lane == 31) misc[warp] = inc;
+    __syncthreads();
+    int base = inc - sum;
+    for (int w = 0; w < warp; ++w) base += misc[w];
+    for (int k = 0; k < each; ++k) {
+        const int b = tid * each + k;
+        if (b >= B) break;
+        off[b] = base;
+        const SeqInfo s = each == 1 ? mine : seq_info(a, b, false);
+        base += nkv * ((s.rows * G + RT - 1) / RT) * span_of<EXTRA>(l, units_of<UNIT>(s));
+        if (b == B - 1) off[B] = base;
+    }
+    __syncthreads();
+    l.total = off[B];
+    return l;
+}
+
+// The task that place u lies in.
+template <int UNIT, int RT, int EXTRA>
+__device__ __forceinline__ void task_at(const AttnPagedArgs &a, const Line &l, const int *off, int u, int &b, int &hr,
+                                        int &units, int &start, int &span, SeqInfo &s) {
+    int lo = 0, hi = a.c.batch;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (off[mid] <= u) lo = mid; else hi = mid;
+    }
+    // (sequences without rows have empty ranges: the last of equal offsets is the one)
+    s = seq_info(a, lo, false);
+    units = units_of<UNIT>(s);
+    span = span_of<EXTRA>(l, units);
+    b = lo;
+    hr = (u - off[lo]) / span;
+    start = off[lo] + hr * span;
+}
+
+// The place at or after u that holds a unit.
+template <int UNIT, int RT, int EXTRA>
+__device__ __forceinline__ int place_from(const AttnPagedArgs &a, const Line &l, const int *off, int u) {
+    if (l.pad || u >= l.total) return u;
+    int b, hr, units, start, span;
+    SeqInfo s;
+    task_at<UNIT, RT, EXTRA>(a, l, off, u, b, hr, units, start, span, s);
+    return u - start < units ? u : start + span;
+}
+
+// The piece that starts at place u of the line (which holds a unit) for a CTA whose places end at
+// u_end; moves u on.
+template <int UNIT, int RT, int EXTRA>
+__device__ __forceinline__ Piece next_piece(const AttnPagedArgs &a, const Line &l, const int *off, int &u,
+                                            int u_end) {
+    const int G = a.nq / a.c.n_kv_heads;
+    int lo, hr, units, start, span;
+    SeqInfo s;
+    task_at<UNIT, RT, EXTRA>(a, l, off, u, lo, hr, units, start, span, s);
+    const int rbs = (s.rows * G + RT - 1) / RT;
+    Piece p;
+    p.b = lo;
+    p.h = hr / rbs;
+    p.r0 = (hr - p.h * rbs) * RT;
+    p.nr = min(RT, s.rows * G - p.r0);
+    p.x0 = u - start;
+    p.x1 = min(units, p.x0 + u_end - u);
+    p.keys = s.total;
+    p.len = s.len;
+    p.first = start / l.per;
+    p.last = (start + units - 1) / l.per;
+    u = p.x1 == units ? start + span : u_end;
+    return p;
+}
+
+// Keys that row r (within the piece's task) may see.
+__device__ __forceinline__ int row_limit(const AttnPagedArgs &a, const Piece &p, int r) {
+    const int G = a.nq / a.c.n_kv_heads;
+    return a.causal ? min(p.keys, p.len + (p.r0 + r) / G + 1) : p.keys;
+}
+
+// Offset of row r's values in q and out.
+__device__ __forceinline__ size_t row_offset(const AttnPagedArgs &a, const Piece &p, int r) {
+    const int G = a.nq / a.c.n_kv_heads, i = (p.r0 + r) / G, g = p.r0 + r - i * G;
+    return (((size_t)p.b * a.blk + i) * a.nq + (size_t)p.h * G + g) * a.c.head_dim;
+}
+
+// Partial result of the k-th CTA of a task: [RT][D] of O, then (m, l) per row. A CTA is the first of
+// at most one task that goes on in others, and a later one of at most one: two places a CTA.
+template <int D, int RT>
+__device__ __forceinline__ float *part_of(const AttnPagedArgs &a, int first, int cta) {
+    return a.part + ((size_t)cta * 2 + (cta == first ? 1 : 0)) * RT * (D + 2);
+}
+
+// The last of a task's CTAs joins the partial results. THREADS threads (tid from 0), sync() their
+// barrier; fac: shared [CTAs of the task][RT], sum: shared [RT], flag: shared; DEPTH parts are loaded
+// together.
+template <int D, int RT, int THREADS, int DEPTH, class Sync>
+__device__ void join_parts(const AttnPagedArgs &a, const Piece &p, int tid, Sync sync, float *fac, float *sum,
+                           int *flag) {
+    const int lane = tid & 31, warp = tid >> 5, cnt = p.last - p.first + 1;
+    __threadfence();
+    sync();
+    if (tid == 0) *flag = atomicAdd(a.counters + p.first, 1) == cnt - 1;
+    sync();
+    if (!*flag) return;
+    __threadfence();
+    if (tid == 0) a.counters[p.first] = 0;
+    for (int rr = warp; rr < p.nr; rr += THREADS / 32) {
+        float mx = -INFINITY;
+        for (int k = lane; k < cnt; k += 32)
+            mx = fmaxf(mx, __ldcg(part_of<D, RT>(a, p.first, p.first + k) + RT * D + 2 * rr));
+        mx = warp_max(mx);
+        float s = 0.f;
+        for (int k = lane; k < cnt; k += 32) {
+            const float2 v = __ldcg(reinterpret_cast<const float2 *>(part_of<D, RT>(a, p.first, p.first + k) + RT * D) + rr);
+            // (a part without a visible key counts 0, unless its sum is a NaN row's NaN)
+            const float f = v.x == -INFINITY ? (v.y == v.y ? 0.f : v.y) : exp2f(v.x - mx);
+            fac[k * RT + rr] = f;
+            s += v.x == -INFINITY ? v.y : v.y * f;
+        }
+        s = warp_sum(s);
+        if (lane == 0) sum[rr] = s;
+    }
+    sync();
+    for (int f = tid; f < p.nr * (D / 4); f += THREADS) {
+        const int rr = f / (D / 4), dim = 4 * (f - rr * (D / 4));
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        // (the first CTA's part is in its second place, the others' in their first)
+        const float *at = part_of<D, RT>(a, p.first, p.first) + rr * D + dim;
+        const float *next = part_of<D, RT>(a, p.first, p.first + 1) + rr * D + dim;
+        for (int k0 = 0; k0 < cnt; k0 += DEPTH) {
+            float4 v[DEPTH];
+#pragma unroll
+            for (int k = 0; k < DEPTH; ++k)
+                if (k0 + k < cnt)
+                    v[k] = __ldcg(reinterpret_cast<const float4 *>(
+                        k0 + k == 0 ? at : next + (size_t)(k0 + k - 1) * 2 * RT * (D + 2)));
+#pragma unroll
+            for (int k = 0; k < DEPTH; ++k) {
+                if (k0 + k >= cnt) break;
+                const float w = fac[(k0 + k) * RT + rr];
+                acc.x = fmaf(v[k].x, w, acc.x);
+                acc.y = fmaf(v[k].y, w, acc.y);
+                acc.z = fmaf(v[k].z, w, acc.z);
+                acc.w = fmaf(v[k].w, w, acc.w);
+            }
+        }
+        const float inv = sum[rr] == 0.f ? 0.f : a.c.v_scale / sum[rr];
+        *reinterpret_cast<float4 *>(a.out + row_offset(a, p, rr) + dim) =
+            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    }
+}
+
+// down = 2^-e and up = 2^e, 2^e the power of two above a row's largest value (1 and 1 for rows of
+// zeros and rows that are not finite; e is kept where both are normal numbers).
+__device__ __forceinline__ void row_scale(float amax, float &down, float &up) {
+    const int bits = __float_as_int(amax) >> 23;               // biased exponent (amax >= 0)
+    const int e = bits == 0 && amax == 0.f ? 0 : (bits == 255 ? 0 : min(max(bits - 126, -125), 126));
+    down = __int_as_float((127 - e) << 23);
+    up = __int_as_float((127 + e) << 23);
+}
+
+// Two values as a pair of FP16 pairs: hi = f16(x), lo = f16(x - hi).
+__device__ __forceinline__ void split_f16(float x0, float x1, uint32_t &hi, uint32_t &lo) {
+    const __half2 h = __floats2half2_rn(x0, x1);
+    const float2 f = __half22float2(h);
+    const __half2 l = __floats2half2_rn(x0 - f.x, x1 - f.y);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    lo = *reinterpret_cast<const uint32_t *>(&l);
+}
+
+__device__ __forceinline__ uint32_t mul_f16(uint32_t a, uint32_t b) {
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// Tensor-core form (k_attn_paged_tc.cu): 0 rows a block if it does not take these sizes.
+struct PagedTcPlan {
+    int np;          // query rows of a block
+    int ctas;
+};
+PagedTcPlan attn_paged_tc_plan(const df_paged_kv &c, int blk, int nq);
+int launch_attn_paged_tc(const AttnPagedArgs &a, const PagedTcPlan &p, cudaStream_t s);
+
+}  // namespace df

@@ -8,7 +8,7 @@
 // value exactly (one conversion and one packed multiply for two values); q (scaled by a power of
 // two to at most 1 a row) and the probabilities enter as FP16 pairs hi + lo, about 22 bits, so a
 // product carries F32's accuracy for two matrix instructions.
-#include "paged.cuh"
+#include "attn_paged.cuh"
 
 namespace df {
 
@@ -17,16 +17,17 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kUnit = 32;        // keys of a warp's step; the unit of the work split
 constexpr int kStages = 2;
+constexpr int kExtra = 24;       // units a piece costs besides its own (8 to 48 measured)
+constexpr int kFlush = 16;       // steps whose products one accumulator takes
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLowest = -3.0e38f;
 constexpr float kLazy = 8.f;     // log2 units a score may exceed its row's reference by
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
-__device__ __forceinline__ void cp16(void *dst, const void *src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src),
-                 "r"(bytes)
-                 : "memory");
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -51,17 +52,6 @@ __device__ __forceinline__ uint32_t movm(uint32_t a) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
     return r;
 }
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ float2 unpack_f16(uint32_t v) {
-    return __half22float2(*reinterpret_cast<const __half2 *>(&v));
-}
-__device__ __forceinline__ uint32_t mul_f16(uint32_t a, uint32_t b) {
-    const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
 // The row (key) a warp's MMA row index stands for, within 16: rows 2t and 2t + 1 are keys t and
 // (t ^ 1) + 4, so that the four keys whose V a thread reads, and the two whose K a quarter-warp
 // reads, lie in different shared-memory banks.
@@ -79,35 +69,10 @@ struct Lay {
     }
 };
 
-// Work split. The keys of every (sequence, KV head, row block) form a line of units of 32 keys;
-// the line is cut into equal pieces, one per CTA, so lengths may be as ragged as they like. A
-// task that lies in several CTAs leaves partial results (O, m, l), joined in CTA order by the
-// last of them to arrive.
 template <int D, int NT>
 constexpr size_t paged_smem(int batch) {
-    return (size_t)kWarps * kStages * Lay<D>::kStage + (size_t)(D / 16) * NT * 32 * 16 +
+    return (size_t)kWarps * (kStages * Lay<D>::kStage + (D / 16) * NT * 512) + (size_t)(D / 16) * NT * 32 * 16 +
            (size_t)kWarps * 8 * NT * 8 + 8 * NT * 16 + 64 * 4 + (size_t)(batch + 1) * 4;
-}
-
-struct SeqInfo {
-    int len, rows, total;        // rows cached before, query rows, keys
-};
-__device__ __forceinline__ SeqInfo seq_info(const AttnPagedArgs &a, int b, bool report) {
-    SeqInfo s;
-    const long long cap = (long long)a.c.max_pages * a.c.page_size;
-    s.len = a.c.seq_len[b];
-    s.rows = a.n_new ? a.n_new[b] : a.blk;
-    if (s.rows < 0 || s.rows > a.blk) {
-        if (report) set_status(a.status, DF_ESHAPE);
-        s.rows = min(max(s.rows, 0), a.blk);
-    }
-    long long t = (long long)s.len + (a.n_new ? s.rows : 0);
-    if (s.len < 0 || t > cap) {
-        if (report) set_status(a.status, DF_ECAPACITY);
-        t = t < 0 ? 0 : (t > cap ? cap : t);
-    }
-    s.total = (int)t;
-    return s;
 }
 
 template <int D, int NT>
@@ -118,7 +83,8 @@ __global__ void __launch_bounds__(32 * kWarps, D * NT <= 128 ? 2 : 1)
     constexpr int RT = 8 * NT, KS = D / 16, MT = D / 16;
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t *ring = smem;
-    uint4 *qf = reinterpret_cast<uint4 *>(ring + kWarps * kStages * L::kStage);   // [KS][NT][32]
+    float4 *sums = reinterpret_cast<float4 *>(ring + kWarps * kStages * L::kStage);   // [kWarps][MT * NT][32]
+    uint4 *qf = reinterpret_cast<uint4 *>(sums + kWarps * MT * NT * 32);          // [KS][NT][32]
     float2 *ml = reinterpret_cast<float2 *>(qf + KS * NT * 32);                   // [kWarps][RT]
     float *rscale = reinterpret_cast<float *>(ml + kWarps * RT);                  // [RT]
     int *rlim = reinterpret_cast<int *>(rscale + RT);                             // [RT]
@@ -128,124 +94,75 @@ __global__ void __launch_bounds__(32 * kWarps, D * NT <= 128 ? 2 : 1)
     int *off = misc + 64;                                                         // [batch + 1]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
-    const int B = a.c.batch, nkv = a.c.n_kv_heads, G = a.nq / nkv;
+    const int nkv = a.c.n_kv_heads;
     const int pshift = 31 - __clz(a.c.page_size);
     pdl_trigger();
     pdl_wait();
-
-    // Units of every sequence, scanned.
-    {
-        const int each = (B + 32 * kWarps - 1) / (32 * kWarps);
-        int sum = 0;
-        for (int k = 0; k < each; ++k) {
-            const int b = tid * each + k;
-            if (b < B) {
-                const SeqInfo s = seq_info(a, b, blockIdx.x == 0);
-                sum += max(1, (s.total + kUnit - 1) / kUnit) * nkv * ((s.rows * G + RT - 1) / RT);
-            }
-        }
-        int inc = sum;
-#pragma unroll
-        for (int m = 1; m < 32; m <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, inc, m);
-            if (lane >= m) inc += o;
-        }
-        if (lane == 31) misc[warp] = inc;
-        __syncthreads();
-        int base = inc - sum;
-        for (int w = 0; w < warp; ++w) base += misc[w];
-        for (int k = 0; k < each; ++k) {
-            const int b = tid * each + k;
-            if (b < B) {
-                off[b] = base;
-                const SeqInfo s = seq_info(a, b, false);
-                base += max(1, (s.total + kUnit - 1) / kUnit) * nkv * ((s.rows * G + RT - 1) / RT);
-                if (b == B - 1) off[B] = base;
-            }
-        }
-        __syncthreads();
-    }
-    const int U = off[B];
-    const int per = max(kWarps / 2, (U + (int)gridDim.x - 1) / (int)gridDim.x);
-    const int u_end = min(U, ((int)blockIdx.x + 1) * per);
-    int u = (int)blockIdx.x * per;
+    const Line line = make_line<kUnit, RT, 32 * kWarps, kExtra>(a, off, misc, 2 * kWarps);
+    const int u_end = min(line.total, ((int)blockIdx.x + 1) * line.per);
+    int u = place_from<kUnit, RT, kExtra>(a, line, off, (int)blockIdx.x * line.per);
 
     while (u < u_end) {
-        // The task of unit u.
-        int lo = 0, hi = B;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (off[mid] <= u) lo = mid; else hi = mid;
-        }
-        // (sequences without rows have empty ranges: the last of equal offsets is the one)
-        const int b = lo;
-        const SeqInfo sq = seq_info(a, b, false);
-        const int units = max(1, (sq.total + kUnit - 1) / kUnit);
-        const int rbs = (sq.rows * G + RT - 1) / RT;
-        const int hr = (u - off[b]) / units;
-        const int h = hr / rbs, rb = hr - h * rbs;
-        const int t_start = off[b] + hr * units;
-        const int x0 = u - t_start, x1 = min(units, x0 + u_end - u);
-        const int r0 = rb * RT, nr = min(RT, sq.rows * G - r0);
+        const Piece p = next_piece<kUnit, RT, kExtra>(a, line, off, u, u_end);
+        const int x0 = p.x0, x1 = p.x1, nr = p.nr;
 
         // Query rows as B fragments: [k step][row tile][lane] = (hi, hi, lo, lo) of four
         // consecutive dims, which are the four that the thread's K fragment holds.
         for (int rr = warp; rr < RT; rr += kWarps) {
             constexpr int GR = D / 4, PER = (GR + 31) / 32;
+            const float unit = kLog2e / sqrtf((float)D);
             float4 v[PER];
             float amax = 0.f;
-            const int r = r0 + rr, i = r / G;
 #pragma unroll
             for (int k = 0; k < PER; ++k) {
                 const int gi = lane + 32 * k;
                 v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (rr < nr && gi < GR)
-                    v[k] = *reinterpret_cast<const float4 *>(
-                        a.q + (((size_t)b * a.blk + i) * a.nq + (size_t)h * G + (r - i * G)) * D + 4 * gi);
+                    v[k] = *reinterpret_cast<const float4 *>(a.q + row_offset(a, p, rr) + 4 * gi);
+                // log2(e) / sqrt(d) is taken into q, so that a row's scale is a power of two
+                v[k].x *= unit;
+                v[k].y *= unit;
+                v[k].z *= unit;
+                v[k].w *= unit;
                 amax = fmaxf(fmaxf(amax, fmaxf(fabsf(v[k].x), fabsf(v[k].y))),
                              fmaxf(fabsf(v[k].z), fabsf(v[k].w)));
             }
             amax = warp_max(amax);
-            int e = 0;
-            if (amax > 0.f && amax <= 3.4028234e38f) frexpf(amax, &e);
+            float down, up;
+            row_scale(amax, down, up);
 #pragma unroll
             for (int k = 0; k < PER; ++k) {
                 const int gi = lane + 32 * k;
                 if (gi >= GR) continue;
-                const float x0f = ldexpf(v[k].x, -e), x1f = ldexpf(v[k].y, -e);
-                const float x2f = ldexpf(v[k].z, -e), x3f = ldexpf(v[k].w, -e);
+                const float x0f = v[k].x * down, x1f = v[k].y * down, x2f = v[k].z * down, x3f = v[k].w * down;
                 uint4 f;
-                f.x = pack_f16(x0f, x1f);
-                f.y = pack_f16(x2f, x3f);
-                const float2 h01 = unpack_f16(f.x), h23 = unpack_f16(f.y);
-                f.z = pack_f16(x0f - h01.x, x1f - h01.y);
-                f.w = pack_f16(x2f - h23.x, x3f - h23.y);
+                split_f16(x0f, x1f, f.x, f.z);
+                split_f16(x2f, x3f, f.y, f.w);
                 int tt, j;
                 if constexpr (D == 64) tt = gi >> 2, j = gi & 3;
                 else tt = (gi & 31) >> 3, j = (gi >> 5) * 8 + (gi & 7);
                 qf[(j * NT + (rr >> 3)) * 32 + (rr & 7) * 4 + tt] = f;
             }
             if (lane == 0) {
-                rscale[rr] = ldexpf(rsqrtf((float)D) * kLog2e * a.c.k_scale, e);
-                rlim[rr] = rr < nr ? (a.causal ? min(sq.total, sq.len + i + 1) : sq.total) : 0;
+                rscale[rr] = a.c.k_scale * up;
+                rlim[rr] = rr < nr ? row_limit(a, p, rr) : 0;
             }
         }
         __syncthreads();
 
         float rs[NT][2];
-        int lim[NT][2], lim_min = 0x7fffffff;
+        int lim_min = 0x7fffffff;
         for (int rr = 0; rr < nr; ++rr) lim_min = min(lim_min, rlim[rr]);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 rs[n][e] = rscale[n * 8 + 2 * t + e];
-                lim[n][e] = rlim[n * 8 + 2 * t + e];
             }
         float o[MT][NT][4], m[NT][2], l[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            m[n][0] = m[n][1] = -INFINITY;
+            m[n][0] = m[n][1] = kLowest;
             l[n][0] = l[n][1] = 0.f;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
@@ -254,46 +171,72 @@ __global__ void __launch_bounds__(32 * kWarps, D * NT <= 128 ? 2 : 1)
         }
 
         uint8_t *my = ring + warp * kStages * L::kStage;
-        const int32_t *table = a.c.page_table + (size_t)b * a.c.max_pages;
-        // Pages of a step's two halves (-1: no rows, or a bad id).
+        const int32_t *table = a.c.page_table + (size_t)p.b * a.c.max_pages;
+        // A step is two groups of 16 rows, each within a page: D / 2 chunks of 16 bytes of K and of V
+        // (PL a lane, at places of its own), and 2 SC of scales, one a lane.
+        constexpr int PL = D / 64, SC = D / 16;
+        const int mask = a.c.page_size - 1, page_rows = nkv << pshift, head_rows = p.h << pshift;
+        const uint32_t my_at = smem_addr(my);
+        uint32_t place[PL];
+#pragma unroll
+        for (int k = 0; k < PL; ++k) {
+            const int c = lane + 32 * k, r = c / L::kChunks;
+            place[k] = r * (D / 2) + (((c % L::kChunks) ^ L::swz(r)) << 4);
+        }
+        const int sc_at = (lane % SC) * 16;
+        const uint8_t *sc_from = (lane < SC ? a.c.k_scales : a.c.v_scales) + sc_at;
+        const uint32_t sc_place = 2 * L::kCodes + (lane < SC ? 0 : L::kScales) + sc_at;
+        // Pages of a step's two groups.
         auto pages_of = [&](int x, int (&pg)[2]) {
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 const int key = x * kUnit + 16 * s;
-                pg[s] = x < x1 && key < sq.total ? table[key >> pshift] : -1;
+                pg[s] = x < x1 && key < p.keys ? table[key >> pshift] : 0;
             }
         };
         auto issue = [&](int x, int stage, const int (&pg)[2]) {
             if (x >= x1) return;
-            uint8_t *st = my + stage * L::kStage;
+            const uint32_t st = my_at + stage * L::kStage;
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                const int key = x * kUnit + 16 * s;
-                const int left = sq.total - key;       // valid rows from here on
-                bool ok = left > 0;
-                if (ok && (pg[s] < 0 || pg[s] >= a.c.n_pages)) {
-                    set_status(a.status, DF_EINVAL);
-                    ok = false;
-                }
-                const size_t row = ok ? (((size_t)pg[s] * nkv + h) << pshift) + (key & (a.c.page_size - 1)) : 0;
+                const int key = x * kUnit + 16 * s, left = p.keys - key;   // valid rows from here on
+                const bool good = (unsigned)pg[s] < (unsigned)a.c.n_pages, ok = good && left > 0;
+                if (!good) set_status(a.status, DF_EINVAL);
+                const size_t row = ok ? (size_t)(unsigned)pg[s] * page_rows + (head_rows + (key & mask)) : 0;
                 if (ok) {
+                    const uint8_t *kc = a.c.k_codes + row * (D / 2) + lane * 16, *vc = a.c.v_codes + row * (D / 2) + lane * 16;
 #pragma unroll
-                    for (int c = lane; c < 16 * L::kChunks; c += 32) {
-                        const int r = c / L::kChunks, ch = c % L::kChunks;
-                        const int to = (16 * s + r) * (D / 2) + ((ch ^ L::swz(r)) << 4);
-                        cp16(st + to, a.c.k_codes + row * (D / 2) + c * 16, 16);
-                        cp16(st + L::kCodes + to, a.c.v_codes + row * (D / 2) + c * 16, 16);
+                    for (int k = 0; k < PL; ++k) {
+                        cp16(st + 16 * s * (D / 2) + place[k], kc + 512 * k, 16);
+                        cp16(st + L::kCodes + 16 * s * (D / 2) + place[k], vc + 512 * k, 16);
                     }
                 }
                 // Scales of rows past the last are zeros, so those rows are zeros whatever the
-                // page holds there.
-                for (int c = lane; c < D / 16; c += 32) {
-                    const int bytes = ok ? min(max(left * (D / 16) - c * 16, 0), 16) : 0;
-                    const size_t at = row * (D / 16) + (bytes ? c * 16 : 0);
-                    cp16(st + 2 * L::kCodes + s * D + c * 16, a.c.k_scales + at, bytes);
-                    cp16(st + 2 * L::kCodes + L::kScales + s * D + c * 16, a.c.v_scales + at, bytes);
+                // page holds.
+                if (lane < 2 * SC) {
+                    const int bytes = ok ? min(max(left * SC - sc_at, 0), 16) : 0;
+                    cp16(st + sc_place + s * D, bytes ? sc_from + row * SC : a.c.k_scales, bytes);
                 }
             }
+        };
+
+        // The tensor core's F32 accumulation rounds towards zero, so a long run of products would
+        // drift: every kFlush steps the outputs join sums in shared memory, rounded to nearest.
+        float4 *mine = sums + warp * MT * NT * 32 + lane;
+        int steps = 0;
+        bool summed = false;
+        auto flush = [&]() {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float4 &f = mine[(mt * NT + n) * 32];
+                    float (&v)[4] = o[mt][n];
+                    f = summed ? make_float4(f.x + v[0], f.y + v[1], f.z + v[2], f.w + v[3]) : make_float4(v[0], v[1], v[2], v[3]);
+                    v[0] = v[1] = v[2] = v[3] = 0.f;
+                }
+            summed = true;
+            steps = 0;
         };
 
         int pg[2];
@@ -327,14 +270,14 @@ __global__ void __launch_bounds__(32 * kWarps, D * NT <= 128 ? 2 : 1)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int r = key_of(g) + 8 * e;
-                        const uint8_t *p = st + (16 * sb + r) * (D / 2);
+                        const uint8_t *pc = st + (16 * sb + r) * (D / 2);
                         const uint8_t *ps = st + 2 * L::kCodes + (16 * sb + r) * (D / 16);
                         if constexpr (D == 64) {
-                            const uint2 w = *reinterpret_cast<const uint2 *>(p + t * 8);
+                            const uint2 w = *reinterpret_cast<const uint2 *>(pc + t * 8);
                             raw[sb][e][0] = w.x, raw[sb][e][1] = w.y;
                             sc[sb][e] = ps[t];
                         } else {
-                            const uint4 w = *reinterpret_cast<const uint4 *>(p + (((t + 4 * c) ^ L::swz(r)) << 4));
+                            const uint4 w = *reinterpret_cast<const uint4 *>(pc + (((t + 4 * c) ^ L::swz(r)) << 4));
                             raw[sb][e][0] = w.x, raw[sb][e][1] = w.y;
                             raw[sb][e][2] = w.z, raw[sb][e][3] = w.w;
                             sc[sb][e] = *reinterpret_cast<const uint16_t *>(ps + 2 * (t + 4 * c));
@@ -373,64 +316,77 @@ __global__ void __launch_bounds__(32 * kWarps, D * NT <= 128 ? 2 : 1)
                     }
                 }
             }
-            // Scores in log2 units; the keys a row may not see drop out.
+            // The keys a row may not see drop out.
             const int key0 = x * kUnit;
-            const bool edge = key0 + kUnit > lim_min;
-            bool over = false;
+            if (key0 + kUnit > lim_min) {
 #pragma unroll
-            for (int sb = 0; sb < 2; ++sb)
+                for (int sb = 0; sb < 2; ++sb)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        s[sb][n][e] *= rs[n][e & 1];
-                        if (edge) {
+                        for (int e = 0; e < 4; ++e) {
                             const int key = key0 + 16 * sb + key_of(g) + 8 * (e >> 1);
-                            if (key >= lim[n][e & 1]) s[sb][n][e] = -INFINITY;
+                            if (key >= rlim[n * 8 + 2 * t + (e & 1)]) s[sb][n][e] = -INFINITY;
                         }
-                        over |= s[sb][n][e] > m[n][e & 1] + kLazy;
+            }
+            // Exponents against the row's reference, in log2 units (rs is a power of two: the
+            // product is exact, and a row's maximum gives 0 against itself however large). The
+            // reference follows the maximum only when a score is kLazy above it, so most steps
+            // neither reduce nor rescale; it starts below any score, and finite, so that a hidden
+            // key's stays -inf against it.
+            float ex[2][NT][4], top = -INFINITY;
+            auto exponents = [&]() {
+#pragma unroll
+                for (int sb = 0; sb < 2; ++sb)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) ex[sb][n][e] = fmaf(s[sb][n][e], rs[n][e & 1], -m[n][e & 1]);
+                        top = fmaxf(top, fmaxf(fmaxf(ex[sb][n][0], ex[sb][n][1]), fmaxf(ex[sb][n][2], ex[sb][n][3])));
                     }
-            // The reference of a row follows its maximum only when a score is kLazy above it, so
-            // most steps neither reduce nor rescale; the results do not depend on it but for
-            // rounding.
-            if (__any_sync(0xffffffffu, over)) {
+            };
+            exponents();
+            if (__any_sync(0xffffffffu, top > kLazy)) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float mx = fmaxf(fmaxf(s[0][n][e], s[0][n][e + 2]), fmaxf(s[1][n][e], s[1][n][e + 2]));
+                        float mx = fmaxf(fmaxf(s[0][n][e], s[0][n][e + 2]), fmaxf(s[1][n][e], s[1][n][e + 2])) * rs[n][e];
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
                         mx = fmaxf(mx, m[n][e]);
-                        const float f = mx == -INFINITY ? 1.f : ex2(m[n][e] - mx);
+                        const float f = ex2(m[n][e] - mx);
                         m[n][e] = mx;
                         l[n][e] *= f;
 #pragma unroll
                         for (int mt = 0; mt < MT; ++mt) {
                             o[mt][n][e] *= f;
                             o[mt][n][e + 2] *= f;
+                            if (summed) {
+                                float *v = reinterpret_cast<float *>(mine + (mt * NT + n) * 32);
+                                v[e] *= f;
+                                v[e + 2] *= f;
+                            }
                         }
                     }
+                exponents();
             }
             uint32_t ph[2][NT][2], pl[2][NT][2];   // P^T as B fragments, hi and lo
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const float m0 = m[n][0] == -INFINITY ? 0.f : m[n][0];
-                const float m1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int sb = 0; sb < 2; ++sb)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float p0 = ex2(s[sb][n][2 * e] - m0), p1 = ex2(s[sb][n][2 * e + 1] - m1);
+                        const float p0 = ex2(ex[sb][n][2 * e]), p1 = ex2(ex[sb][n][2 * e + 1]);
                         l[n][0] += p0;
                         l[n][1] += p1;
-                        const uint32_t hh = pack_f16(p0, p1);
-                        const float2 hf = unpack_f16(hh);
+                        uint32_t hh, ll;
+                        split_f16(p0, p1, hh, ll);
                         ph[sb][n][e] = movm(hh);
-                        pl[sb][n][e] = movm(pack_f16(p0 - hf.x, p1 - hf.y));
+                        pl[sb][n][e] = movm(ll);
                     }
-            }
             // O^T += V^T P^T: a thread holds d / 8 consecutive dims of four keys; nibbles of two
             // keys are interleaved so that one conversion gives a pair of keys.
             constexpr int VW = D / 64;             // words of a thread's dims
@@ -440,17 +396,17 @@ __global__ void __launch_bounds__(32 * kWarps, D * NT <= 128 ? 2 : 1)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int r = ((e & 1) ? (t ^ 1) + 4 : t) + 8 * (e >> 1);
-                    const uint8_t *p = st + L::kCodes + (16 * sb + r) * (D / 2);
+                    const uint8_t *pc = st + L::kCodes + (16 * sb + r) * (D / 2);
                     const uint8_t *ps = st + 2 * L::kCodes + L::kScales + (16 * sb + r) * (D / 16);
                     if constexpr (D == 64) {
-                        raw[e][0] = *reinterpret_cast<const uint32_t *>(p + g * 4);
+                        raw[e][0] = *reinterpret_cast<const uint32_t *>(pc + g * 4);
                         sv[e] = ps[g >> 1];
                     } else if constexpr (D == 128) {
-                        const uint2 w = *reinterpret_cast<const uint2 *>(p + (((g >> 1) ^ L::swz(r)) << 4) + (g & 1) * 8);
+                        const uint2 w = *reinterpret_cast<const uint2 *>(pc + (((g >> 1) ^ L::swz(r)) << 4) + (g & 1) * 8);
                         raw[e][0] = w.x, raw[e][1] = w.y;
                         sv[e] = ps[g];
                     } else {
-                        const uint4 w = *reinterpret_cast<const uint4 *>(p + ((g ^ L::swz(r)) << 4));
+                        const uint4 w = *reinterpret_cast<const uint4 *>(pc + ((g ^ L::swz(r)) << 4));
                         raw[e][0] = w.x, raw[e][1] = w.y, raw[e][2] = w.z, raw[e][3] = w.w;
                         sv[e] = *reinterpret_cast<const uint16_t *>(ps + 2 * g);
                     }
@@ -484,6 +440,7 @@ __global__ void __launch_bounds__(32 * kWarps, D * NT <= 128 ? 2 : 1)
                     }
                 }
             }
+            if (++steps == kFlush) flush();
             __syncwarp();
             issue(x + kStages * kWarps, stage, pg);
             cp_commit();
@@ -491,6 +448,18 @@ __global__ void __launch_bounds__(32 * kWarps, D * NT <= 128 ? 2 : 1)
             stage = stage + 1 == kStages ? 0 : stage + 1;
         }
         cp_wait<0>();
+        if (summed) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const float4 f = mine[(mt * NT + n) * 32];
+                    o[mt][n][0] += f.x;
+                    o[mt][n][1] += f.y;
+                    o[mt][n][2] += f.z;
+                    o[mt][n][3] += f.w;
+                }
+        }
 
         // Join the warps: every warp's O^T tiles go to shared memory (over the ring), then every
         // thread sums its elements over the warps, scaled to the common reference.
@@ -513,21 +482,19 @@ __global__ void __launch_bounds__(32 * kWarps, D * NT <= 128 ? 2 : 1)
                 ob[(warp * MT * NT + mt * NT + n) * 32 + lane] =
                     make_float4(o[mt][n][0], o[mt][n][1], o[mt][n][2], o[mt][n][3]);
         if (tid < RT) {
-            float mx = -INFINITY, sum = 0.f;
+            float mx = kLowest, sum = 0.f;
             for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, ml[w * RT + tid].x);
             for (int w = 0; w < kWarps; ++w) {
-                const float2 v = ml[w * RT + tid];
-                const float f = v.x == -INFINITY ? 0.f : ex2(v.x - mx);
-                sum += v.x == -INFINITY ? v.y : v.y * f;   // (0 then, or NaN of a NaN row)
-                ml[w * RT + tid].x = v.x == -INFINITY && v.y == v.y ? 0.f : (v.x == -INFINITY ? v.y : f);
+                const float f = ex2(ml[w * RT + tid].x - mx);
+                sum += ml[w * RT + tid].y * f;
+                ml[w * RT + tid].x = f;
             }
             rm[tid] = mx;
             rl[tid] = sum;
         }
         __syncthreads();
-        const int c_first = t_start / per, c_last = (t_start + units - 1) / per;
-        const bool whole = c_first == c_last;
-        float *part = a.part + ((size_t)blockIdx.x * 2 + ((int)blockIdx.x == c_first ? 1 : 0)) * RT * (D + 2);
+        const bool whole = p.whole();
+        float *part = part_of<D, RT>(a, p.first, (int)blockIdx.x);
         for (int f = tid; f < MT * NT * 32; f += 32 * kWarps) {
             const int ln = f & 31, tile = f >> 5, n = tile % NT, mt = tile / NT;
             const int ra = n * 8 + 2 * (ln & 3), dim = (ln >> 2) * (D / 8) + 2 * mt;
@@ -548,10 +515,9 @@ __global__ void __launch_bounds__(32 * kWarps, D * NT <= 128 ? 2 : 1)
                 float2 v = e ? make_float2(acc.y, acc.w) : make_float2(acc.x, acc.z);
                 if (whole) {
                     const float inv = rl[rr] == 0.f ? 0.f : a.c.v_scale / rl[rr];
-                    const int r = r0 + rr, i = r / G;
                     v.x *= inv;
                     v.y *= inv;
-                    *reinterpret_cast<float2 *>(a.out + (((size_t)b * a.blk + i) * a.nq + (size_t)h * G + (r - i * G)) * D + dim) = v;
+                    *reinterpret_cast<float2 *>(a.out + row_offset(a, p, rr) + dim) = v;
                 } else {
                     *reinterpret_cast<float2 *>(part + rr * D + dim) = v;
                 }
@@ -562,57 +528,10 @@ __global__ void __launch_bounds__(32 * kWarps, D * NT <= 128 ? 2 : 1)
                 part[RT * D + 2 * tid] = rm[tid];
                 part[RT * D + 2 * tid + 1] = rl[tid];
             }
-            __threadfence();
-            __syncthreads();
-            // (a CTA is the first of at most one task that goes on in others)
-            const int cnt = c_last - c_first + 1;
-            if (tid == 0) misc[32] = atomicAdd(a.counters + c_first, 1) == cnt - 1;
-            __syncthreads();
-            if (misc[32]) {
-                // The last of the task's CTAs joins the partial results, in CTA order.
-                __threadfence();
-                if (tid == 0) a.counters[c_first] = 0;
-                auto at = [&](int k) {
-                    return a.part + ((size_t)(c_first + k) * 2 + (k == 0 ? 1 : 0)) * RT * (D + 2);
-                };
-                float *fac = reinterpret_cast<float *>(ring);          // [cnt][RT]
-                float *sum = reinterpret_cast<float *>(ml);            // [RT]
-                for (int rr = warp; rr < nr; rr += kWarps) {
-                    float mx = -INFINITY;
-                    for (int k = lane; k < cnt; k += 32) mx = fmaxf(mx, __ldcg(at(k) + RT * D + 2 * rr));
-                    mx = warp_max(mx);
-                    float s = 0.f;
-                    for (int k = lane; k < cnt; k += 32) {
-                        const float mk = __ldcg(at(k) + RT * D + 2 * rr), lk = __ldcg(at(k) + RT * D + 2 * rr + 1);
-                        const float f = mk == -INFINITY ? (lk == lk ? 0.f : lk) : ex2(mk - mx);
-                        fac[k * RT + rr] = f;
-                        s += mk == -INFINITY ? lk : lk * f;
-                    }
-                    s = warp_sum(s);
-                    if (lane == 0) sum[rr] = s;
-                }
-                __syncthreads();
-                for (int f = tid; f < nr * (D / 4); f += 32 * kWarps) {
-                    const int rr = f / (D / 4), dim = 4 * (f - rr * (D / 4));
-                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                    for (int k = 0; k < cnt; ++k) {
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(at(k) + rr * D + dim));
-                        const float w = fac[k * RT + rr];
-                        acc.x = fmaf(v.x, w, acc.x);
-                        acc.y = fmaf(v.y, w, acc.y);
-                        acc.z = fmaf(v.z, w, acc.z);
-                        acc.w = fmaf(v.w, w, acc.w);
-                    }
-                    const float inv = sum[rr] == 0.f ? 0.f : a.c.v_scale / sum[rr];
-                    const int r = r0 + rr, i = r / G;
-                    *reinterpret_cast<float4 *>(a.out + (((size_t)b * a.blk + i) * a.nq + (size_t)h * G + (r - i * G)) * D + dim) =
-                        make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-                }
-            }
+            join_parts<D, RT, 32 * kWarps, (D == 256 ? 16 : 8)>(a, p, tid, [] { __syncthreads(); }, reinterpret_cast<float *>(ring),
+                                           reinterpret_cast<float *>(ml), misc + 32);
         }
         __syncthreads();
-        u += x1 - x0;
     }
 }
 
@@ -622,7 +541,7 @@ struct Plan {
 Plan plan_of(const df_paged_kv &c, int blk, int nq) {
     Plan p;
     const int rows = blk * (nq / c.n_kv_heads);
-    p.nt = rows <= 8 ? 1 : 2;
+    p.nt = rows <= 8 || c.head_dim == 256 ? 1 : 2;
     p.rt = 8 * p.nt;
     p.rb = (rows + p.rt - 1) / p.rt;
     p.ctas = sm_count() * (c.head_dim * p.nt <= 128 ? 2 : 1);
@@ -639,19 +558,22 @@ int launch_one(const AttnPagedArgs &a, const Plan &p, cudaStream_t s) {
 }  // namespace
 
 size_t attn_paged_part_floats(const df_paged_kv &c, int blk, int nq) {
+    const PagedTcPlan t = attn_paged_tc_plan(c, blk, nq);
+    if (t.np) return (size_t)t.ctas * 2 * t.np * (c.head_dim + 2);
     const Plan p = plan_of(c, blk, nq);
     return (size_t)p.ctas * 2 * p.rt * (c.head_dim + 2);
 }
 
 int launch_attn_paged(const AttnPagedArgs &a, cudaStream_t s) {
+    const PagedTcPlan t = attn_paged_tc_plan(a.c, a.blk, a.nq);
+    if (t.np) return launch_attn_paged_tc(a, t, s);
     const Plan p = plan_of(a.c, a.blk, a.nq);
     switch (a.c.head_dim * 4 + p.nt) {
         case 64 * 4 + 1: return launch_one<64, 1>(a, p, s);
         case 64 * 4 + 2: return launch_one<64, 2>(a, p, s);
         case 128 * 4 + 1: return launch_one<128, 1>(a, p, s);
         case 128 * 4 + 2: return launch_one<128, 2>(a, p, s);
-        case 256 * 4 + 1: return launch_one<256, 1>(a, p, s);
-        default: return launch_one<256, 2>(a, p, s);
+        default: return launch_one<256, 1>(a, p, s);
     }
 }
 

@@ -1,0 +1,804 @@
+// Attention over the paged 4-bit KV cache on the 5th-generation tensor cores.
+//
+// The products of k_attn_paged.cu, S^T = K Q^T and O^T = V^T P^T, as tcgen05 MMAs of 128 keys (128
+// dims) by 2 NP columns: the hi halves of the NP query rows, then the lo halves, so one MMA a K step
+// carries both and the sum is taken when the accumulator is read. A persistent CTA of
+//   loading warps       q as the B operand of a piece; the keys' codes and scales into a ring
+//   converting warps    a thread is one key (128 dims of one, of V): 4-bit codes times scale, exactly
+//                       FP16; K into tensor memory (the A operand of S^T), V into shared memory
+//                       as it lies, dims contiguous (the A operand of O^T, M-major)
+//   2 MMA warps         one thread each issues the scores' and the outputs' products
+//   2 softmax groups    of 4 warps (8 for 32 rows) that take the 128-key tiles in turn: a thread is
+//                       one key (and half the rows): scores from tensor memory, probabilities to
+//                       shared memory (the B operand of O^T, N-major)
+// so that no operand is transposed, and rows cost matrix columns instead of instructions. A tile's
+// softmax is a chain of latencies (scores, exponentials, stores, fences: about 1 us); the two
+// groups have references, sums and outputs of their own, so two such chains run side by side, and
+// are joined at the end of a piece.
+//
+// O^T accumulates in tensor memory for at most kFlush tiles of a group, then joins an F32 sum in
+// shared memory: long sums are rounded there, and a row whose maximum rises rescales there.
+#include "attn_paged.cuh"
+#include "tc_ptx.cuh"
+
+namespace df {
+
+namespace {
+
+constexpr int kTile = 128;                   // keys of a tile
+constexpr int kTmemCols = 512;
+constexpr int kExtra = 8;                    // tiles a piece costs besides its own (2 to 16 measured)
+constexpr int kFlush = 8;
+// Log2 units a score may exceed its row's reference by: a probability is at most 2^15, an FP16.
+constexpr float kMost = 15.f;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLowest = -3.0e38f;
+
+template <int D, int NP>
+struct Cfg {
+    static constexpr int kHalves = D / 128;                   // 128-dim halves of a row
+    static constexpr int kSplit = NP == 32 ? 2 : 1;           // threads of a key in a softmax group
+    static constexpr int kGroupWarps = 4 * kSplit;
+    // Warps, in this order: one thread is a key of K, or 128 dims of a key of V. (More threads for
+    // either cost more registers than they bring: with 8 warps for V 162 instead of 146 us for 8
+    // sequences of 32768 keys, 32 rows a head.)
+    static constexpr int kKWarps = 4, kVWarps = 4 * kHalves;
+    static constexpr int kSoftWarp = kKWarps + kVWarps, kMmaWarp = kSoftWarp + 2 * kGroupWarps;
+    static constexpr int kLoadWarp = kMmaWarp + 2, kLoadWarps = 4;
+    static constexpr int kThreads = 32 * (kLoadWarp + kLoadWarps);
+    static constexpr int kCodes = kTile * D / 2;              // bytes of a tile's K (or V) codes
+    static constexpr int kScales = kTile * D / 16;
+    static constexpr int kRaw = 2 * kCodes + 2 * kScales;
+    // As deep as shared memory allows: a tile's bytes are 2 to 3 us on their way.
+    static constexpr int kRawStages = D == 128 ? (NP == 32 ? 4 : 5) : 2;
+    static constexpr int kVBytes = kTile * 128 * 2;           // 128 dims of a tile's V, FP16
+    static constexpr int kVBufs = 2;
+    static constexpr int kPBytes = kTile * 128;               // a tile's P: 128-byte rows
+    static constexpr int kQBytes = 2 * NP * D * 2;
+    static constexpr int kQBufs = D == 128 && NP < 32 ? 2 : 1;
+    static constexpr int kAccBytes = 2 * NP * D * 4;          // F32 outputs: [group][row][D]
+    static constexpr int kBars = 2 * kRawStages + 2 + 2 * kVBufs + 2 + 2 + 2 + 2 + 2 * kQBufs + 2;
+    static constexpr size_t kFixed = 1024 + (size_t)kVBufs * kVBytes + 2 * kPBytes + kQBufs * kQBytes +
+                                     kRawStages * kRaw + kAccBytes + kBars * 8 + 64 * 4 +
+                                     (size_t)NP * 4 * (4 * kQBufs + 8 + 2 + 2) + 64;
+    // TMEM columns: two K operands, two score tiles, the groups' outputs
+    static constexpr int kKCols = D / 2;
+    static constexpr int kS = 2 * kKCols, kO = kS + 4 * NP, kOCols = kHalves * 2 * NP;
+    static_assert(kO + 2 * kOCols <= kTmemCols, "tensor memory");
+    static_assert(kFixed <= 232448 - 1028, "shared memory (256 sequences at least)");
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<unsigned long long &>(r))
+        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<unsigned long long &>(r))
+        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)),
+          "l"(reinterpret_cast<unsigned long long &>(c)));
+    return r;
+}
+// Barriers of the softmax warps: of one group (1 or 2), and of both (3).
+template <int THREADS>
+__device__ __forceinline__ void named_sync(int id) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(THREADS) : "memory");
+}
+template <int THREADS>
+__device__ __forceinline__ bool named_sync_or(int id, bool p) {
+    uint32_t r;
+    asm volatile(
+        "{\n .reg .pred a, b;\n setp.ne.u32 a, %1, 0;\n barrier.cta.red.or.pred b, %3, %2, a;\n"
+        " selp.u32 %0, 1, 0, b;\n}\n"
+        : "=r"(r)
+        : "r"((uint32_t)p), "n"(THREADS), "r"(id)
+        : "memory");
+    return r != 0;
+}
+// min that keeps a NaN
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+// M- or N-major operand stored as 128-byte rows of 64 values, one row a K index, 128-byte swizzle:
+// groups of 8 rows 1024 bytes apart, the next 64 values 16 KB on.
+__device__ __forceinline__ uint64_t mn_desc(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(16384 >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[N]) {
+    if constexpr (N == 4) {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(taddr));
+    } else if constexpr (N == 8) {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                       "=r"(r[7])
+                     : "r"(taddr));
+    } else {
+        static_assert(N == 16, "rows of a thread");
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+            "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+              "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+            : "r"(taddr));
+    }
+}
+__device__ __forceinline__ void tmem_load_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// Reduces N values a lane over the warp's lanes, halving the values at every step; the result of
+// value `row` is in every lane (lanes of equal `row` hold the same).
+template <int N, bool MAX>
+__device__ __forceinline__ float reduce_rows(float (&v)[N], int lane, int &row) {
+    row = 0;
+    int o = 16;
+#pragma unroll
+    for (int n = N; n > 1; n >>= 1, o >>= 1) {
+        const bool up = (lane & o) != 0;
+#pragma unroll
+        for (int i = 0; i < n / 2; ++i) {
+            const float keep = up ? v[i + n / 2] : v[i], send = up ? v[i] : v[i + n / 2];
+            const float got = __shfl_xor_sync(0xffffffffu, send, o);
+            v[i] = MAX ? fmaxf(keep, got) : keep + got;
+        }
+        if (up) row += n / 2;
+    }
+    float r = v[0];
+    for (; o >= 1; o >>= 1) {
+        const float got = __shfl_xor_sync(0xffffffffu, r, o);
+        r = MAX ? fmaxf(r, got) : r + got;
+    }
+    return r;
+}
+
+template <int D, int NP>
+__global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1) attn_paged_tc_kernel(const __grid_constant__ AttnPagedArgs a) {
+    DF_TRACE_KERNEL(TK_ATTN_PAGED);
+    using C = Cfg<D, NP>;
+    constexpr int HR = NP / C::kSplit, CR = 8;                 // rows of a softmax thread, of one step
+    constexpr int kSoftWarp = C::kSoftWarp, kMmaWarp = C::kMmaWarp, kLoadWarps = C::kLoadWarps;
+    constexpr int kSoftWarps = 2 * C::kGroupWarps, kGroupThreads = 32 * C::kGroupWarps;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    uint8_t *vbuf = smem;
+    uint8_t *pbuf = vbuf + C::kVBufs * C::kVBytes;
+    uint8_t *qbuf = pbuf + 2 * C::kPBytes;
+    uint8_t *raw = qbuf + C::kQBufs * C::kQBytes;
+    float *accs = reinterpret_cast<float *>(raw + C::kRawStages * C::kRaw);
+    uint64_t *bar = reinterpret_cast<uint64_t *>(reinterpret_cast<uint8_t *>(accs) + C::kAccBytes);
+    uint64_t *raw_full = bar, *raw_free = raw_full + C::kRawStages;
+    uint64_t *k_full = raw_free + C::kRawStages;               // [2] K operand in tensor memory
+    uint64_t *v_full = k_full + 2, *v_free = v_full + C::kVBufs;
+    uint64_t *qk_done = v_free + C::kVBufs;                    // [2] scores ready, K operand free
+    uint64_t *s_free = qk_done + 2, *p_full = s_free + 2;      // [2] each
+    uint64_t *pv_done = p_full + 2;                            // [2] outputs added, P free
+    uint64_t *q_full = pv_done + 2, *q_free = q_full + C::kQBufs;
+    uint64_t *drain = q_free + C::kQBufs;                      // [2]
+    int *misc = reinterpret_cast<int *>(drain + 2);            // [64]
+    float *rscale = reinterpret_cast<float *>(misc + 64);      // [kQBufs][NP]
+    int *rlim = reinterpret_cast<int *>(rscale + C::kQBufs * NP);
+    size_t *roff = reinterpret_cast<size_t *>(rlim + C::kQBufs * NP);   // row_offset of every row
+    float *red = reinterpret_cast<float *>(roff + C::kQBufs * NP);      // [2 groups][4][NP]
+    float *ref = red + 8 * NP, *rl = ref + 2 * NP;             // [2][NP] negatives of the references; [2][NP] sums
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(rl + 2 * NP);
+    int *abort_flag = reinterpret_cast<int *>(tslot + 1);
+    int *acc_flag = abort_flag + 1;                            // [2] whether tile n's P V adds up
+    int *flag = acc_flag + 2;
+    int *off = flag + 1;                                       // [batch + 1]
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int nkv = a.c.n_kv_heads, pshift = 31 - __clz(a.c.page_size);
+
+    if (tid == 0) {
+        for (int i = 0; i < C::kRawStages; ++i) {
+            mbar_init(&raw_full[i], 32 * kLoadWarps);
+            mbar_init(&raw_free[i], C::kKWarps + C::kVWarps);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&k_full[i], 4);
+            mbar_init(&qk_done[i], 1);
+            mbar_init(&s_free[i], C::kGroupWarps);
+            mbar_init(&p_full[i], C::kGroupWarps);
+            mbar_init(&pv_done[i], 1);
+        }
+        for (int i = 0; i < C::kVBufs; ++i) {
+            mbar_init(&v_full[i], 4);
+            mbar_init(&v_free[i], 1);
+        }
+        for (int i = 0; i < C::kQBufs; ++i) {
+            mbar_init(&q_full[i], kLoadWarps);
+            mbar_init(&q_free[i], kSoftWarps);
+        }
+        mbar_init(&drain[0], 1);
+        mbar_init(&drain[1], 1);
+        *abort_flag = 0;
+
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(tslot, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    pdl_trigger();
+    pdl_wait();
+    const Line line = make_line<kTile, NP, C::kThreads, kExtra>(a, off, misc, 1);   // (its barriers cover the set-up)
+    tc_fence_after();
+    const uint32_t tmem = *tslot;
+    const int u_end = min(line.total, ((int)blockIdx.x + 1) * line.per);
+    int u = place_from<kTile, NP, kExtra>(a, line, off, (int)blockIdx.x * line.per);
+    auto wait = [&](uint64_t *b, int phase) {
+        return mbar_try_wait(b, (uint32_t)(phase & 1)) || mbar_wait(b, (uint32_t)(phase & 1), abort_flag, a.status);
+    };
+
+    if (warp >= C::kLoadWarp) {
+        // ---- loading warps
+        const int lw = warp - C::kLoadWarp;
+        // 16 rows of a page are D / 2 chunks of 16 bytes, contiguous; a lane's chunks lie at places of
+        // their own in every group of 16 rows (chunk c of row r at c ^ swizzle(r), as the
+        // converting warps read them).
+        constexpr int CH = D / 32, PL = D / 64, SC = D / 16;   // chunks of a row; of a lane; of scales
+        uint32_t place[PL];
+#pragma unroll
+        for (int i = 0; i < PL; ++i) {
+            const int c = lane + 32 * i, r = c / CH, ch = c % CH;
+            place[i] = r * (D / 2) + ((D == 128 ? ch ^ ((r >> 1) & 3) : ch ^ (r & 7)) << 4);
+        }
+        int n = 0, seg = 0;                                    // tiles, pieces so far
+        while (u < u_end) {
+            const Piece p = next_piece<kTile, NP, kExtra>(a, line, off, u, u_end);
+            const int32_t *table = a.c.page_table + (size_t)p.b * a.c.max_pages;
+            // Lane g of 8 holds the page of a tile's 16-row group g (-1: no rows).
+            auto pages = [&](int x) {
+                const int key = x * kTile + 16 * (lane & 7);
+                return x < p.x1 && key < p.keys ? table[key >> pshift] : -1;
+            };
+            int page = pages(p.x0);
+            const int qb = seg % C::kQBufs;
+            if (seg >= C::kQBufs) wait(&q_free[qb], seg / C::kQBufs - 1);
+            uint8_t *qs = qbuf + qb * C::kQBytes;
+            // A warp's rows, QR loaded at a time; lane k looks after row k of them.
+            constexpr int WR = NP / kLoadWarps, QR = WR < 4 ? WR : 4;
+            const int mine = lw * WR + (lane < WR ? lane : 0);
+            const size_t my_off = mine < p.nr ? row_offset(a, p, mine) : 0;
+            float my_up = 1.f;
+            // log2(e) / sqrt(d) is taken into q, so that a row's scale is a power of two
+            const float unit = kLog2e / sqrtf((float)D);
+            auto scaled = [&](float4 f) { return make_float4(f.x * unit, f.y * unit, f.z * unit, f.w * unit); };
+            for (int k0 = 0; k0 < WR; k0 += QR) {
+                float4 v[QR][D / 128];
+#pragma unroll
+                for (int k = 0; k < QR; ++k) {
+                    const float *src = a.q + __shfl_sync(0xffffffffu, my_off, k0 + k) + 4 * lane;
+#pragma unroll
+                    for (int hf = 0; hf < D / 128; ++hf) {
+                        v[k][hf] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (lw * WR + k0 + k < p.nr) v[k][hf] = scaled(*reinterpret_cast<const float4 *>(src + 128 * hf));
+                    }
+                }
+                float amax[QR];
+#pragma unroll
+                for (int k = 0; k < QR; ++k) {
+                    amax[k] = 0.f;
+#pragma unroll
+                    for (int hf = 0; hf < D / 128; ++hf)
+                        amax[k] = fmaxf(fmaxf(amax[k], fmaxf(fabsf(v[k][hf].x), fabsf(v[k][hf].y))),
+                                        fmaxf(fabsf(v[k][hf].z), fabsf(v[k][hf].w)));
+                }
+#pragma unroll
+                for (int m = 16; m >= 1; m >>= 1)
+#pragma unroll
+                    for (int k = 0; k < QR; ++k) amax[k] = fmaxf(amax[k], __shfl_xor_sync(0xffffffffu, amax[k], m));
+#pragma unroll
+                for (int k = 0; k < QR; ++k) {
+                    const int rr = lw * WR + k0 + k;
+                    float down, up;
+                    row_scale(amax[k], down, up);
+                    if (lane == k0 + k) my_up = up;
+#pragma unroll
+                    for (int hf = 0; hf < D / 128; ++hf) {
+                        uint2 h, lo;
+                        split_f16(v[k][hf].x * down, v[k][hf].y * down, h.x, lo.x);
+                        split_f16(v[k][hf].z * down, v[k][hf].w * down, h.y, lo.y);
+                        // dims 128 hf + 4 lane .. + 3 of rows rr (hi) and NP + rr (lo)
+                        uint8_t *o = qs + (2 * hf + (lane >> 4)) * (2 * NP * 128) + rr * 128 +
+                                     (((((lane & 15) >> 1)) ^ (rr & 7)) << 4) + (lane & 1) * 8;
+                        *reinterpret_cast<uint2 *>(o) = h;
+                        *reinterpret_cast<uint2 *>(o + NP * 128) = lo;   // (NP is a multiple of 8)
+                    }
+                }
+            }
+            if (lane < WR) {
+                rscale[qb * NP + mine] = a.c.k_scale * my_up;
+                rlim[qb * NP + mine] = mine < p.nr ? row_limit(a, p, mine) : 0;
+                roff[qb * NP + mine] = my_off;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_full[qb]);
+            for (int x = p.x0; x < p.x1; ++x, ++n) {
+                const int st = n % C::kRawStages;
+                const int now = page;
+                page = pages(x + 1);
+                if (n >= C::kRawStages) wait(&raw_free[st], n / C::kRawStages - 1);
+                const uint32_t to = smem_u32(raw + st * C::kRaw);
+                if (now >= a.c.n_pages || (now < 0 && x * kTile + 16 * (lane & 7) < p.keys)) set_status(a.status, DF_EINVAL);
+                const bool good = now >= 0 && now < a.c.n_pages;
+                const int key = x * kTile + 16 * (lane & 7);
+                // first row of the group in the pools (-1: none), for lanes 0 to 7
+                const long long row = good ? ((((long long)now * nkv + p.h) << pshift) + (key & (a.c.page_size - 1))) : -1;
+#pragma unroll 1
+                for (int i = 0; i < 8 / kLoadWarps; ++i) {
+                    const int grp = lw + kLoadWarps * i;
+                    const long long at = __shfl_sync(0xffffffffu, row, grp);
+                    const size_t from = (size_t)(at < 0 ? 0 : at) * (D / 2) + lane * 16;
+                    const uint32_t dst = to + grp * (16 * D / 2);
+                    if (at >= 0) {
+#pragma unroll
+                        for (int k = 0; k < PL; ++k) {
+                            cp16(dst + place[k], a.c.k_codes + from + 512 * k, 16);
+                            cp16(dst + C::kCodes + place[k], a.c.v_codes + from + 512 * k, 16);
+                        }
+                    }
+                    // Scales: D bytes a group of K, then of V; zeros past the last row, so those
+                    // rows are zeros whatever the page holds.
+                    if (lane < 2 * SC) {
+                        const int c = lane % SC, left = p.keys - (x * kTile + 16 * grp);
+                        const int bytes = at < 0 ? 0 : min(max(left * SC - c * 16, 0), 16);
+                        const size_t sf = (size_t)(at < 0 ? 0 : at) * SC + (bytes ? c * 16 : 0);
+                        cp16(to + 2 * C::kCodes + (lane < SC ? 0 : C::kScales) + grp * D + c * 16,
+                             (lane < SC ? a.c.k_scales : a.c.v_scales) + sf, bytes);
+                    }
+                }
+                cp_arrive(&raw_full[st]);
+            }
+            ++seg;
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp >= kMmaWarp) {
+        // ---- MMA warps, one for the scores and one for the outputs: every lane follows, one elected
+        // lane issues. The descriptors of a K step are those of the first plus a constant (with each
+        // built anew in a loop an MMA took 0.1 us to issue, and a tile's 16 of them more than all
+        // else that a tile needs). A wait on a barrier, even one that is long complete, costs some
+        // 200 cycles here, so one warp for both products (four waits a tile) held the tiles up.
+        const bool issue = elect_one();
+        const uint32_t id_qk = (1u << 4) | ((uint32_t)(2 * NP >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+        const uint32_t id_pv = id_qk | (1u << 15) | (1u << 16);
+        const bool outputs = warp > kMmaWarp;
+        int n = 0, seg = 0;
+        bool ok = true;
+        while (u < u_end && ok) {
+            const Piece p = next_piece<kTile, NP, kExtra>(a, line, off, u, u_end);
+            if (!outputs) {
+                const int qb = seg % C::kQBufs;
+                const uint64_t bq = sw128_desc(smem_u32(qbuf + qb * C::kQBytes));
+                ok = ok && wait(&q_full[qb], seg / C::kQBufs);
+                for (int x = p.x0; x < p.x1 && ok; ++x, ++n) {
+                    if (n >= 2) ok = wait(&s_free[n & 1], (n >> 1) - 1);
+                    ok = ok && wait(&k_full[n & 1], n >> 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (issue) {
+#pragma unroll
+                        for (int s = 0; s < D / 16; ++s)
+                            mma_bf16_ts(tmem + C::kS + (n & 1) * 2 * NP, tmem + (n & 1) * C::kKCols + 8 * s,
+                                        bq + (((s >> 2) * (2 * NP * 128) + (s & 3) * 32) >> 4), id_qk, s ? 1u : 0u);
+                        mma_commit(&qk_done[n & 1]);
+                    }
+                }
+            } else {
+                for (int x = p.x0; x < p.x1 && ok; ++x, ++n) {
+                    const uint64_t bp = mn_desc(smem_u32(pbuf + (n & 1) * C::kPBytes));
+                    uint32_t add = 0;
+#pragma unroll
+                    for (int hf = 0; hf < C::kHalves; ++hf) {
+                        const int v = n * C::kHalves + hf, vb = v % C::kVBufs;
+                        ok = ok && wait(&v_full[vb], v / C::kVBufs);
+                        if (hf == 0) {
+                            ok = ok && wait(&p_full[n & 1], n >> 1);
+                            add = reinterpret_cast<volatile int *>(acc_flag)[n & 1] != 0;
+                        }
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t av = mn_desc(smem_u32(vbuf + vb * C::kVBytes));
+                        if (issue) {
+#pragma unroll
+                            for (int s = 0; s < kTile / 16; ++s)
+                                mma_bf16(tmem + C::kO + (n & 1) * C::kOCols + hf * 2 * NP, av + (2048 >> 4) * s,
+                                         bp + (2048 >> 4) * s, id_pv, s ? 1u : add);
+                            mma_commit(&v_free[vb]);
+                            if (hf == C::kHalves - 1) mma_commit(&pv_done[n & 1]);
+                        }
+                    }
+                }
+            }
+            ++seg;
+        }
+        // Every MMA issued has completed once this barrier flips.
+        if (issue) {
+            mma_commit(&drain[outputs]);
+            mbar_drain(&drain[outputs], 0);
+        }
+        __syncwarp();
+    } else if (warp < kSoftWarp) {
+        // ---- converting warps: key 32 (warp % 4) + lane; of V, dims [128 half, + 128)
+        const bool is_k = warp < C::kKWarps;
+        const int key = 32 * (warp & 3) + lane, half = is_k ? 0 : (warp - C::kKWarps) >> 2;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint8_t *row = raw + key * (D / 2);
+        auto chunk = [&](int c) { return (D == 128 ? c ^ ((key >> 1) & 3) : c ^ (key & 7)) << 4; };
+        // Eight dims of word w as FP16, times the scale of its block of 16 (word pair).
+        auto convert = [](uint32_t w, uint32_t scales, int blk, uint32_t (&f)[4]) {
+            e2m1x8_to_f16(w, f);
+            const uint32_t s2 = __byte_perm(scales, 0, blk & 1 ? 0x3232 : 0x1010);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] = mul_f16(f[e], s2);
+        };
+        // A ring of two stages (D = 256) is freed early: a tile's words are held in registers, where
+        // the waits for the operand's buffer follow (104 instead of 117 us for 8 sequences of 32768
+        // keys, 12 rows a head). A deep ring has no need of it, and its loops stay rolled: the roles'
+        // code shares the instruction caches (161 instead of 173 us for 32 rows of D = 128).
+        constexpr bool kHeld = C::kRawStages == 2;
+        constexpr int kK = kHeld ? D / 32 : 1, kV = kHeld ? 4 : 1;
+        int n = 0;
+        while (u < u_end) {
+            const Piece p = next_piece<kTile, NP, kExtra>(a, line, off, u, u_end);
+            for (int x = p.x0; x < p.x1; ++x, ++n) {
+                const int st = n % C::kRawStages;
+                wait(&raw_full[st], n / C::kRawStages);
+                const uint8_t *r = row + st * C::kRaw;
+                const uint8_t *sc = raw + st * C::kRaw + 2 * C::kCodes + key * (D / 16);
+                auto codes = [&](int c) { return *reinterpret_cast<const uint4 *>(r + chunk(c)); };
+                auto scales = [&](int c) { return e4m3x2_to_f16(*reinterpret_cast<const uint16_t *>(sc + 2 * c)); };
+                auto freed = [&]() {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&raw_free[st]);
+                };
+                if (is_k) {
+                    uint4 held[kK];
+                    uint32_t held_s[kK];
+                    if constexpr (kHeld) {
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c) held[c] = codes(c), held_s[c] = scales(c);
+                        freed();
+                    }
+                    if (n >= 2) wait(&qk_done[n & 1], (n >> 1) - 1);
+                    tc_fence_after();
+#pragma unroll kK
+                    for (int c = 0; c < D / 32; ++c) {
+                        const uint4 w = kHeld ? held[c] : codes(c);
+                        const uint32_t s = kHeld ? held_s[c] : scales(c);
+                        const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+                        uint32_t o[16];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t f[4];
+                            convert(in[k], s, k / 2, f);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[4 * k + e] = f[e];
+                        }
+                        tmem_st16(tmem + lanes + (n & 1) * C::kKCols + 16 * c, o);
+                    }
+                    if (!kHeld) freed();
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&k_full[n & 1]);
+                } else {
+                    // 128 dims are two 64-wide blocks of the operand.
+                    r += C::kCodes;
+                    sc += C::kScales;
+                    uint4 held[kV];
+                    uint32_t held_s[kV];
+                    if constexpr (kHeld) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) held[c] = codes(4 * half + c), held_s[c] = scales(4 * half + c);
+                        freed();
+                    }
+                    const int unit = n * C::kHalves + half, vb = unit % C::kVBufs;
+                    if (unit >= C::kVBufs) wait(&v_free[vb], unit / C::kVBufs - 1);
+                    uint8_t *vo = vbuf + vb * C::kVBytes + key * 128;
+#pragma unroll kV
+                    for (int c = 0; c < 4; ++c) {
+                        const uint4 w = kHeld ? held[c] : codes(4 * half + c);
+                        const uint32_t s = kHeld ? held_s[c] : scales(4 * half + c);
+                        const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t f[4];
+                            convert(in[k], s, k / 2, f);
+                            *reinterpret_cast<uint4 *>(vo + (c >> 1) * 16384 + ((((4 * c + k) & 7) ^ (key & 7)) << 4)) =
+                                make_uint4(f[0], f[1], f[2], f[3]);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&v_full[vb]);
+                    if (!kHeld) freed();
+                }
+            }
+        }
+    } else {
+        // ---- softmax warps: group grp takes tiles of its parity. A thread is key
+        // 32 (warp % 4) + lane of a tile (a dim, of the outputs) and rows [r0, r0 + HR).
+        const int sw = warp - kSoftWarp, grp = sw / C::kGroupWarps, gt = tid - 32 * (kSoftWarp + grp * C::kGroupWarps);
+        const int lq = warp & 3, r0 = C::kSplit == 2 ? ((sw >> 2) & 1) * HR : 0, kt = 32 * lq + lane;
+        const int st_id = tid - 32 * kSoftWarp;
+        const uint32_t lanes = (uint32_t)(32 * lq) << 16;
+        float *gred = red + grp * 4 * NP, *gref = ref + grp * NP;
+        const float2 *nm = reinterpret_cast<const float2 *>(gref + r0);
+        auto group_sync = [&] { named_sync<kGroupThreads>(1 + grp); };
+        auto all_sync = [&] { named_sync<32 * kSoftWarps>(3); };
+        int n = 0, seg = 0;
+        while (u < u_end) {
+            const Piece p = next_piece<kTile, NP, kExtra>(a, line, off, u, u_end);
+            const int qb = seg % C::kQBufs;
+            // Sums of pairs of rows; the references' negatives are one for the group and lie in
+            // shared memory: at first a value below any score, finite so that a masked score
+            // stays -inf against it.
+            float2 l[HR / 2];
+            auto acc = [&](int hf, int r) -> float & { return accs[(grp * NP + r0 + r) * D + 128 * hf + kt]; };
+#pragma unroll
+            for (int i = 0; i < HR / 2; ++i) l[i] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int hf = 0; hf < C::kHalves; ++hf)
+#pragma unroll
+                for (int i = 0; i < HR; ++i) acc(hf, i) = 0.f;
+            if (gt < NP) gref[gt] = -kLowest;
+            wait(&q_full[qb], seg / C::kQBufs);
+            const float2 *rs2 = reinterpret_cast<const float2 *>(rscale + qb * NP + r0);
+            const int *lim = rlim + qb * NP + r0;
+            int lim_min = 0x7fffffff;
+            for (int r = 0; r < p.nr; ++r) lim_min = min(lim_min, rlim[qb * NP + r]);
+            int pending = 0, mine = 0;                         // tiles in the TMEM outputs; tiles so far
+            // Tiles up to i join the F32 sums.
+            auto flush = [&](int i) {
+                if (pending == 0) return;
+                wait(&pv_done[grp], i >> 1);
+                tc_fence_after();
+#pragma unroll
+                for (int hf = 0; hf < C::kHalves; ++hf) {
+                    const uint32_t to = tmem + lanes + C::kO + grp * C::kOCols + hf * 2 * NP + r0;
+#pragma unroll
+                    for (int c = 0; c < HR; c += CR) {
+                        uint32_t h[CR], lo[CR];
+                        tmem_load<CR>(to + c, h);
+                        tmem_load<CR>(to + NP + c, lo);
+                        tmem_load_wait();
+#pragma unroll
+                        for (int r = 0; r < CR; ++r) acc(hf, c + r) += __uint_as_float(h[r]) + __uint_as_float(lo[r]);
+                    }
+                }
+                pending = 0;
+            };
+            const int n0 = n;
+            for (int x = p.x0 + ((n0 & 1) != grp ? 1 : 0); x < p.x1; x += 2) {
+                const int i = n0 + x - p.x0, par = i >> 1;     // tile; the use of the group's buffers
+                wait(&qk_done[grp], par);
+                tc_fence_after();
+                const uint32_t ts = tmem + lanes + C::kS + grp * 2 * NP + r0;
+                const int key = x * kTile + kt;
+                const bool edge = (x + 1) * kTile > lim_min;
+                // Scores of rows [c, c + CR), to be scaled by rs2.
+                auto scores = [&](int c, float2 (&s)[CR / 2]) {
+                    uint32_t h[CR], lo[CR];
+                    tmem_load<CR>(ts + c, h);
+                    tmem_load<CR>(ts + NP + c, lo);
+                    tmem_load_wait();
+#pragma unroll
+                    for (int r = 0; r < CR / 2; ++r) {
+                        s[r] = add2(make_float2(__uint_as_float(h[2 * r]), __uint_as_float(h[2 * r + 1])),
+                                    make_float2(__uint_as_float(lo[2 * r]), __uint_as_float(lo[2 * r + 1])));
+                        if (edge) {
+                            if (key >= lim[c + 2 * r]) s[r].x = -INFINITY;
+                            if (key >= lim[c + 2 * r + 1]) s[r].y = -INFINITY;
+                        }
+                    }
+                };
+                // The references rise to the maxima of this tile.
+                auto rise = [&]() {
+#pragma unroll
+                    for (int c = 0; c < HR; c += CR) {
+                        float2 s[CR / 2];
+                        scores(c, s);
+                        float mx[CR];
+#pragma unroll
+                        for (int r = 0; r < CR / 2; ++r) {
+                            mx[2 * r] = s[r].x * rs2[c / 2 + r].x;
+                            mx[2 * r + 1] = s[r].y * rs2[c / 2 + r].y;
+                        }
+                        int row;
+                        const float high = reduce_rows<CR, true>(mx, lane, row);
+                        gred[lq * NP + r0 + c + row] = high;
+                    }
+                    flush(i - 2);
+                    group_sync();
+                    auto raised = [&](int r) {
+                        return fmaxf(fmaxf(fmaxf(gred[r], gred[NP + r]), fmaxf(gred[2 * NP + r], gred[3 * NP + r])), -gref[r]);
+                    };
+                    const float top = gt < NP ? raised(gt) : 0.f;
+#pragma unroll
+                    for (int r = 0; r < HR; ++r) {
+                        const float f = ex2(-gref[r0 + r] - raised(r0 + r));
+                        float &lr = r & 1 ? l[r / 2].y : l[r / 2].x;
+                        lr *= f;
+#pragma unroll
+                        for (int hf = 0; hf < C::kHalves; ++hf) acc(hf, r) *= f;
+                    }
+                    group_sync();
+                    if (gt < NP) gref[gt] = -top;
+                    group_sync();
+                };
+                if (mine == 0) rise();
+                else if (pending == kFlush) flush(i - 2);
+                if (par > 0) wait(&pv_done[grp], par - 1);     // (the P buffer is free)
+                uint8_t *po = pbuf + grp * C::kPBytes + kt * 128;
+                // Probabilities to shared memory. The exponents against the reference are bounded
+                // by kMost; where one was above, the tile is taken again against raised
+                // references (its probabilities leave the sums first: sign -1).
+                auto probabilities = [&](float sign) {
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < HR; c += CR) {
+                        float2 e[CR / 2];
+                        scores(c, e);
+                        uint32_t ph[CR / 2], pl[CR / 2];
+#pragma unroll
+                        for (int r = 0; r < CR / 2; ++r) {
+                            // (rs2 are powers of two: the product is exact, so a row's maximum
+                            // gives 0 against itself however large its scores)
+                            e[r] = fma2(e[r], rs2[c / 2 + r], nm[c / 2 + r]);
+                            top = fmaxf(top, fmaxf(e[r].x, e[r].y));
+                            e[r] = make_float2(ex2(min_nan(e[r].x, kMost)), ex2(min_nan(e[r].y, kMost)));
+                            float2 &lr = l[c / 2 + r];
+                            lr = fma2(e[r], make_float2(sign, sign), lr);
+                            split_f16(e[r].x, e[r].y, ph[r], pl[r]);
+                        }
+                        if (sign > 0.f) {
+                            const int ch = (r0 + c) >> 3;      // 16-byte piece of the row
+                            *reinterpret_cast<uint4 *>(po + ((ch ^ (kt & 7)) << 4)) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
+                            *reinterpret_cast<uint4 *>(po + (((ch + NP / 8) ^ (kt & 7)) << 4)) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
+                        }
+                    }
+                    return top;
+                };
+                const bool over = probabilities(1.f) > kMost;
+                if (mine > 0 && named_sync_or<kGroupThreads>(1 + grp, over)) {
+                    probabilities(-1.f);
+                    rise();
+                    probabilities(1.f);
+                }
+                if (gt == 0) acc_flag[grp] = pending > 0;
+                ++pending;
+                ++mine;
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&s_free[grp]);
+                    mbar_arrive(&p_full[grp]);
+                }
+            }
+            n = n0 + p.x1 - p.x0;
+            // The group's last tile is the last of its parity.
+            if (mine > 0) flush(((n - 1) & 1) == grp ? n - 1 : n - 2);
+            tc_fence_before();
+            // Row sums over the keys' lanes and quarters.
+#pragma unroll
+            for (int c = 0; c < HR; c += CR) {
+                float ls[CR];
+#pragma unroll
+                for (int r = 0; r < CR; ++r) ls[r] = r & 1 ? l[(c + r) / 2].y : l[(c + r) / 2].x;
+                int row;
+                const float sum = reduce_rows<CR, false>(ls, lane, row);
+                gred[lq * NP + r0 + c + row] = sum;
+            }
+            group_sync();
+            if (gt < NP) rl[grp * NP + gt] = gred[gt] + gred[NP + gt] + gred[2 * NP + gt] + gred[3 * NP + gt];
+            all_sync();
+            // The groups' results joined: every thread takes its dims of every other row.
+            float *part = part_of<D, NP>(a, p.first, (int)blockIdx.x);
+            const size_t *row_of = roff + qb * NP;
+            auto factors = [&](int r, float &f0, float &f1) {
+                const float m0 = -ref[r], m1 = -ref[NP + r], m = fmaxf(m0, m1);
+                f0 = ex2(m0 - m);
+                f1 = ex2(m1 - m);
+                return rl[r] * f0 + rl[NP + r] * f1;
+            };
+            for (int r = grp * C::kSplit + (r0 ? 1 : 0); r < p.nr; r += 2 * C::kSplit) {
+                float f0, f1;
+                const float L = factors(r, f0, f1), inv = p.whole() ? (L == 0.f ? 0.f : a.c.v_scale / L) : 1.f;
+                float *to = p.whole() ? a.out + row_of[r] : part + r * D;
+#pragma unroll
+                for (int hf = 0; hf < C::kHalves; ++hf) {
+                    const int d = 128 * hf + kt;
+                    to[d] = (accs[r * D + d] * f0 + accs[(NP + r) * D + d] * f1) * inv;
+                }
+            }
+            if (!p.whole()) {
+                if (st_id < NP) {
+                    float f0, f1;
+                    part[NP * D + 2 * st_id + 1] = factors(st_id, f0, f1);
+                    part[NP * D + 2 * st_id] = fmaxf(-ref[st_id], -ref[NP + st_id]);
+                }
+                // The factors of the join (one a CTA of the task and row) take the P buffers:
+                // every P V has completed.
+                join_parts<D, NP, 32 * kSoftWarps, 4>(a, p, st_id, all_sync, reinterpret_cast<float *>(pbuf), red, flag);
+            }
+            all_sync();
+            if (lane == 0) mbar_arrive(&q_free[qb]);
+            ++seg;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <int D, int NP>
+int launch_one(const AttnPagedArgs &a, int ctas, cudaStream_t s) {
+    return launch_k("attn_paged_tc_kernel", attn_paged_tc_kernel<D, NP>, dim3(ctas), dim3(Cfg<D, NP>::kThreads),
+                    Cfg<D, NP>::kFixed + (size_t)(a.c.batch + 1) * 4, s, a);
+}
+
+constexpr size_t kMaxSmem = 232448;
+
+}  // namespace
+
+// More than 8 query rows a head over enough keys: rows cost this kernel matrix columns and the other
+// one instructions, but a CTA's first outputs take some 10 us longer here. Measured, the other
+// kernel : this one in us, at rows a head x keys a CTA, 8 heads of K and V:
+//   D = 128   8 x 13800  87 : 114   16 x 860  26 : 26   16 x 3450  46 : 43   16 x 13800  136 : 119
+//             32 x 430   21 : 25    32 x 860  32 : 35   32 x 1725  44 : 38   32 x 13800  238 : 148
+//   D = 256   8 x 13800  143 : 188  16 x 860  33 : 37   16 x 1725  46 : 44   16 x 13800  271 : 195
+//             32 x 215   23 : 23    32 x 860  53 : 50   64 x 110   26 : 32   64 x 3450   270 : 193
+// which crosses where rows x D x keys a CTA are some 4M. Keys are counted by the page table's width,
+// which is what a launch knows of them.
+PagedTcPlan attn_paged_tc_plan(const df_paged_kv &c, int blk, int nq) {
+    const int rows = blk * (nq / c.n_kv_heads), ctas = sm_count() < kOpsCounters ? sm_count() : kOpsCounters;
+    const double keys = (double)c.batch * c.n_kv_heads * c.max_pages * c.page_size / ctas;
+    PagedTcPlan p{0, ctas};
+    if (rows <= 8 || c.head_dim == 64 || keys * rows * c.head_dim < 4e6) return p;
+    p.np = c.head_dim == 256 || rows <= 16 ? 16 : 32;
+    const size_t fixed = c.head_dim == 256 ? Cfg<256, 16>::kFixed : p.np == 16 ? Cfg<128, 16>::kFixed : Cfg<128, 32>::kFixed;
+    if (fixed + (size_t)(c.batch + 1) * 4 > kMaxSmem) p.np = 0;
+    return p;
+}
+
+int launch_attn_paged_tc(const AttnPagedArgs &a, const PagedTcPlan &p, cudaStream_t s) {
+    if (a.c.head_dim == 256) return launch_one<256, 16>(a, p.ctas, s);
+    return p.np == 16 ? launch_one<128, 16>(a, p.ctas, s) : launch_one<128, 32>(a, p.ctas, s);
+}
+
+}  // namespace df

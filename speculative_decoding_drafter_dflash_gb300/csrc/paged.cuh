@@ -28,12 +28,23 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t w) {
     return r;
 }
 
-// (lo, hi) rounded to E2M1 (nearest even, at most 6): lo in bits 0-3, hi in bits 4-7.
-__device__ __forceinline__ uint32_t f32x2_to_e2m1(float lo, float hi) {
+// x rounded to E2M1 (nearest even, at most 6), as 4 bits of a byte.
+__device__ __forceinline__ uint32_t f32_to_e2m1(float x) {
     uint32_t r;
-    asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\tcvt.u32.u8 %0, b;\n\t}"
+    asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %1;\n\tcvt.u32.u8 %0, b;\n\t}"
         : "=r"(r)
-        : "f"(lo), "f"(hi));
+        : "f"(x));
+    return r & 0xfu;
+}
+// Four values rounded to E2M1, the first in the lowest 4 bits of 16.
+__device__ __forceinline__ uint32_t f32x4_to_e2m1(float x0, float x1, float x2, float x3) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, z;\n\tmov.b32 {z, z, z, z}, 0;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "mov.b32 %0, {a, b, z, z};\n\t}"
+        : "=r"(r)
+        : "f"(x0), "f"(x1), "f"(x2), "f"(x3));
     return r;
 }
 

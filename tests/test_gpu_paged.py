@@ -35,12 +35,17 @@ def _i32(x):
 class Pool:
     """A cache whose pages are a shuffled part of the pool, every byte set to a pattern first."""
 
-    def __init__(self, lens, extra, nkv, d, page, seed=0, fill=0xAB, k_scale=1.0, v_scale=1.0):
+    def __init__(self, lens, extra, nkv, d, page, seed=0, fill=0xAB, k_scale=1.0, v_scale=1.0, rows=0):
+        """rows: query rows a head that the page table is so wide for that the attention takes its
+        kernel for long contexts (the width is what it counts keys by)."""
         rng = np.random.default_rng(seed)
         need = [-(-(n + e) // page) for n, e in zip(lens, extra)]
         pages = sum(need) + 3
         ids = rng.permutation(pages)[:sum(need)]
-        self.table = np.full((len(lens), max(max(need), 1)), -1, dtype=np.int32)
+        width = max(max(need), 1)
+        if rows:
+            width = max(width, -(-10 ** 7 * 152 // (rows * d * nkv * page * len(lens))))
+        self.table = np.full((len(lens), width), -1, dtype=np.int32)
         at = 0
         for b, n in enumerate(need):
             self.table[b, :n] = ids[at:at + n]
@@ -359,10 +364,28 @@ ATTEND = [
 ]
 
 
-@pytest.mark.parametrize("case", ATTEND)
-def test_attention_matches_float64(case):
+# (more than 8 rows a head of 128 or 256, which the kernel for long contexts takes)
+LONG = [
+    ([64], [5], 5, 4, 2, 128, 16, False),
+    ([0], [9], 9, 2, 2, 128, 16, True),
+    ([0], None, 16, 1, 1, 128, 128, False),
+    ([1, 15, 16, 17, 127, 128, 129, 0], None, 3, 16, 4, 128, 16, False),
+    ([0, 3, 128, 255], [16, 0, 3, 11], 16, 6, 3, 128, 32, True),
+    ([2100], [16], 16, 4, 2, 128, 16, True),
+    ([513, 7], [2, 2], 2, 12, 1, 256, 128, True),
+    ([90, 0, 400], [12, 12, 0], 12, 4, 4, 256, 16, True),
+    ([1300], None, 3, 24, 4, 256, 256, False),
+    ([0, 40], [70, 33], 70, 2, 2, 128, 32, True),
+    ([500, 129], [30, 7], 30, 3, 1, 256, 64, True),
+    (list(range(0, 200, 5)), [1] * 40, 1, 36, 2, 128, 64, True),
+    ([9000], [8], 8, 8, 2, 128, 256, True),
+]
+
+
+@pytest.mark.parametrize("case,long", [(c, False) for c in ATTEND + LONG] + [(c, True) for c in LONG])
+def test_attention_matches_float64(case, long):
     lens, n_new, blk, nq, nkv, d, page, causal = case
-    pool = Pool(lens, n_new or [0] * len(lens), nkv, d, page, seed=2)
+    pool = Pool(lens, n_new or [0] * len(lens), nkv, d, page, seed=2, rows=blk * (nq // nkv) if long else 0)
     keep, pool.lens = pool.lens, [n + (0 if n_new is None else n_new[i]) for i, n in enumerate(pool.lens)]
     host = pool.fill_random(5)
     pool.lens = keep
@@ -375,8 +398,12 @@ def test_attention_matches_float64(case):
     assert np.all(np.abs(got - ref) <= tol), (np.abs(got - ref).max(), tol.max())
 
 
-def _small(lens=(40, 20), n_new=(3, 2), nq=4, nkv=2, d=128, page=16, seed=7):
-    pool = Pool(lens, n_new, nkv, d, page, seed)
+# the tests below, for both kernels: 6 rows a head, and 18 or 12 of a wide table
+BOTH = pytest.mark.parametrize("shape", [{}, dict(nq=12, long=True), dict(nq=8, d=256, long=True)])
+
+
+def _small(lens=(40, 20), n_new=(3, 2), nq=4, nkv=2, d=128, page=16, seed=7, long=False):
+    pool = Pool(lens, n_new, nkv, d, page, seed, rows=max(n_new) * nq // nkv if long else 0)
     pool.lens = [a + b for a, b in zip(lens, n_new)]
     host = pool.fill_random(seed)
     pool.lens = list(lens)
@@ -384,8 +411,9 @@ def _small(lens=(40, 20), n_new=(3, 2), nq=4, nkv=2, d=128, page=16, seed=7):
     return pool, host, q
 
 
-def test_attention_does_not_see_what_lies_behind_the_last_row():
-    pool, host, q = _small()
+@BOTH
+def test_attention_does_not_see_what_lies_behind_the_last_row(shape):
+    pool, host, q = _small(**shape)
     for t in pool.pools():
         t.fill_(0x7F)                       # NaN scales everywhere ...
     want = None
@@ -404,8 +432,9 @@ def test_attention_does_not_see_what_lies_behind_the_last_row():
         want = got
 
 
-def test_attention_rows_of_q_that_are_not_finite_stay_alone():
-    pool, host, q = _small()
+@BOTH
+def test_attention_rows_of_q_that_are_not_finite_stay_alone(shape):
+    pool, host, q = _small(**shape)
     ref, tol = _attend_ref(pool, host, q, [3, 2], False)
     q[0, 1, 2, 7], q[1, 0, 0, 3] = np.nan, np.inf
     got = _attend(pool, torch.tensor(q, device=DEV), _i32([3, 2]), False).cpu().numpy()
@@ -415,10 +444,11 @@ def test_attention_rows_of_q_that_are_not_finite_stay_alone():
     assert np.all((np.abs(got - ref) <= tol)[~bad])
 
 
+@BOTH
 @pytest.mark.parametrize("size", [1e-30, 1e-3, 1e4, 1e30])
-def test_attention_of_q_of_any_size(size):
+def test_attention_of_q_of_any_size(size, shape):
     # tiny q: a plain mean; huge q: the keys of the largest score alone, however far above F16
-    pool, host, q = _small(seed=9)
+    pool, host, q = _small(seed=9, **shape)
     q = (q * np.float32(size)).astype(np.float32)
     got = _attend(pool, torch.tensor(q, device=DEV), _i32([3, 2]), False).cpu().numpy()
     ref, tol = _attend_ref(pool, host, q, [3, 2], False)
@@ -428,10 +458,11 @@ def test_attention_of_q_of_any_size(size):
     assert np.all(np.abs(got - ref) <= tol), np.abs(got - ref).max()
 
 
-def test_attention_late_and_early_maxima():
+@pytest.mark.parametrize("heads", [1, 3, 6])
+def test_attention_late_and_early_maxima(heads):
     # scores that rise by far more than the lazy margin along the keys, and that fall
     for order in (1, -1):
-        pool = Pool([600], [0], 1, 128, 64)
+        pool = Pool([600], [0], 1, 128, 64, rows=4 * heads if heads > 1 else 0)
         host = pool.host()
         rng = np.random.default_rng(11)
         u = rng.standard_normal(128)
@@ -440,15 +471,16 @@ def test_attention_late_and_early_maxima():
             pool.put(host, 0, r, (u * at / 60)[None], rng.standard_normal((1, 128)))
         for t, a in zip(pool.pools(), host):
             t.copy_(torch.tensor(a))
-        q = np.stack([u * f for f in (0.1, 1.0, -1.0, 5.0)])[None, None].astype(np.float32)
+        q = np.stack([u * f for f in (0.1, 1.0, -1.0, 5.0) * heads])[None, None].astype(np.float32)
         got = _attend(pool, torch.tensor(q, device=DEV), None, False).cpu().numpy()
         ref, tol = _attend_ref(pool, host, q, None, False)
         assert np.all(np.abs(got - ref) <= tol), np.abs(got - ref).max()
 
 
-def test_attention_bad_tables_and_lengths_reach_the_status():
+@BOTH
+def test_attention_bad_tables_and_lengths_reach_the_status(shape):
     for what in ("page", "length", "negative", "count"):
-        pool, host, q = _small()
+        pool, host, q = _small(**shape)
         n_new = [3, 2]
         if what == "page":
             pool.cache.page_table[0, 1] = 1 << 24
@@ -465,10 +497,11 @@ def test_attention_bad_tables_and_lengths_reach_the_status():
         assert np.all(np.abs(got[1] - ref[1]) <= tol[1]), what
 
 
-def test_attention_repeats_bit_for_bit_and_shares_a_workspace_between_sizes():
-    pool, host, q = _small(lens=(3000, 2999), n_new=(4, 4), seed=13)
+@pytest.mark.parametrize("nq", [4, 12])
+def test_attention_repeats_bit_for_bit_and_shares_a_workspace_between_sizes(nq):
+    pool, host, q = _small(lens=(3000, 2999), n_new=(4, 4), nq=nq, seed=13, long=nq > 4)
     other, ohost, oq = _small(lens=(50,), n_new=(20,), nq=8, nkv=1, d=64, seed=14)
-    need = max(B.attention_paged_workspace_bytes(pool.cache, 4, 4),
+    need = max(B.attention_paged_workspace_bytes(pool.cache, 4, nq),
                B.attention_paged_workspace_bytes(other.cache, 20, 8), B.token_logprobs_workspace_bytes(3, 9000, 2))
     ws = B.alloc_workspace(need)
     qt, oqt = torch.tensor(q, device=DEV), torch.tensor(oq, device=DEV)
@@ -489,12 +522,13 @@ def test_attention_repeats_bit_for_bit_and_shares_a_workspace_between_sizes():
     assert float((first[2] - want).abs().max()) <= 2.0 ** -18 + 2.0 ** -22 * float(want.abs().max())
 
 
-def test_two_streams_and_a_captured_graph():
-    pool, host, q = _small(lens=(700, 650), n_new=(2, 2), seed=15)
+@pytest.mark.parametrize("nq", [4, 20])
+def test_two_streams_and_a_captured_graph(nq):
+    pool, host, q = _small(lens=(700, 650), n_new=(2, 2), nq=nq, seed=15, long=nq > 4)
     n = _i32([2, 2])
     qt = torch.tensor(q, device=DEV)
     ref, tol = _attend_ref(pool, host, q, [2, 2], True)
-    size = B.attention_paged_workspace_bytes(pool.cache, 2, 4)
+    size = B.attention_paged_workspace_bytes(pool.cache, 2, nq)
     ws = [B.alloc_workspace(size) for _ in range(3)]
     outs = [torch.zeros_like(qt) for _ in range(3)]
     torch.cuda.synchronize()

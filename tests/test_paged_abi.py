@@ -161,12 +161,10 @@ def test_binding_refuses_what_the_kernels_would_misread(L):
     table, n = torch.zeros((2, 4), dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
     with pytest.raises(TypeError, match="^k_codes: expected a contiguous CUDA torch.uint8"):
         L.PagedKv(u, s, u, s, table, n)
-    with pytest.raises(ValueError, match="do not fit"):
-        L.PagedKv(u, s[:, :, :, :4], u, s, table, n)
-    with pytest.raises(ValueError, match="do not fit"):
-        L.PagedKv(u, s, u, s, table, n[:1])
-    with pytest.raises(TypeError, match="^k: expected a CUDA"):
-        L._rows(f, 2, 3, 256, "k")
+    with pytest.raises(TypeError, match="^k: expected a contiguous CUDA"):
+        L._rows(f, 0, (2, 3, 256), "k")
+    with pytest.raises(TypeError, match="^seq_len: expected a contiguous CUDA"):
+        L.kv_advance(n, n, 8)
     with pytest.raises(TypeError, match="^logits: expected CUDA"):
         L.token_logprobs(torch.zeros((2, 8)), n, torch.zeros(2))
     assert torch.equal(L.rope_frequencies(1e4, 4, "cpu"), torch.tensor([1.0, 1e-2], dtype=torch.float64))
