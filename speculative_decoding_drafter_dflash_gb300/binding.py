@@ -690,21 +690,36 @@ def generate(model: "DFlashModel", ref, agree, table, sel, prior_cap, prior_len,
 U8, F64 = torch.uint8, torch.float64
 
 
-def _same_device(cache, *tensors):
-    """The calls below run on the cache's device, on that device's current stream: a tensor of
-    another device raises here."""
-    for t in tensors:
-        if t is not None and t.device != cache.device:
-            raise ValueError(f"a tensor on {t.device}, the first on {cache.device}")
+def _arg(t, dtype, dev: int, shape, name: str):
+    """Address of a contiguous tensor of `dtype` and `shape` on CUDA device `dev` (None passes
+    through); anything else raises here rather than reaching a kernel that would misread it."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        raise _misfit(t, dtype, dev, shape, name)
+    return t.data_ptr()
 
 
-def _run(device, stream, fn, *args):
-    """fn(*args, stream) with `device` current (the library launches on the current device)."""
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)))
-    else:
-        with torch.cuda.device(device):
-            _check(fn(*args, _stream(stream)))
+def _misfit(t, dtype, dev, shape, name):
+    want = f"{name}: expected a contiguous CUDA {dtype} tensor {list(shape)} on cuda:{dev}"
+    got = (f"got {t.dtype} {list(t.shape)} on {t.device}"
+           + ("" if t.is_contiguous() else f" with strides {t.stride()}"))
+    return (TypeError if t.dtype is not dtype or not t.is_cuda else ValueError)(f"{want}, {got}")
+
+
+def _launch(dev: int, stream, fn, *args):
+    """fn(*args, stream), on `dev`'s current stream unless one is given, with `dev` current (the
+    library launches on the current device, the tensors are all on `dev`)."""
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _launch(dev, stream, fn, *args)
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    rc = fn(*args, stream)
+    if rc != DF_OK:
+        _check(rc)
 
 
 class PagedKv:
@@ -716,23 +731,23 @@ class PagedKv:
                  k_scale: float = 1.0, v_scale: float = 1.0):
         n_pages, n_kv, page, half = k_codes.shape
         B, max_pages = page_table.shape
-        if (k_codes.shape != v_codes.shape or k_scales.shape != v_scales.shape
-                or tuple(k_scales.shape) != (n_pages, n_kv, page, half // 8)
-                or tuple(seq_len.shape) != (B,)):
-            raise ValueError("codes [pages, kv, page, d / 2], scales [pages, kv, page, d / 16], "
-                             "page_table [B, max pages] and seq_len [B] do not fit together")
-        self.k_codes, self.k_scales, self.v_codes, self.v_scales = (k_codes, k_scales, v_codes,
-                                                                    v_scales)
-        self.page_table, self.seq_len = page_table, seq_len
-        self.device = k_codes.device
-        self.batch, self.n_kv, self.head_dim = B, n_kv, 2 * half
-        self.cap = max_pages * page
-        self.c = PagedKvC(_dev(k_codes, U8, "k_codes"), _dev(v_codes, U8, "v_codes"),
-                          _dev(k_scales, U8, "k_scales"), _dev(v_scales, U8, "v_scales"),
-                          _dev(page_table, I32, "page_table"), _dev(seq_len, I32, "seq_len"),
+        dev = k_codes.get_device()
+        codes, scales = (n_pages, n_kv, page, half), (n_pages, n_kv, page, half // 8)
+        if dev < 0:
+            raise _misfit(k_codes, U8, 0, codes, "k_codes")
+        self.c = PagedKvC(_arg(k_codes, U8, dev, codes, "k_codes"),
+                          _arg(v_codes, U8, dev, codes, "v_codes"),
+                          _arg(k_scales, U8, dev, scales, "k_scales"),
+                          _arg(v_scales, U8, dev, scales, "v_scales"),
+                          _arg(page_table, I32, dev, (B, max_pages), "page_table"),
+                          _arg(seq_len, I32, dev, (B,), "seq_len"),
                           n_pages, page, max_pages, B, n_kv, 2 * half, k_scale, v_scale)
+        self.k_codes, self.k_scales = k_codes, k_scales
+        self.v_codes, self.v_scales = v_codes, v_scales
+        self.page_table, self.seq_len = page_table, seq_len
+        self.dev, self.batch, self.n_kv, self.head_dim = dev, B, n_kv, 2 * half
+        self.cap = max_pages * page
         self.ref = ctypes.byref(self.c)
-        _same_device(self, k_scales, v_codes, v_scales, page_table, seq_len)
 
     @classmethod
     def empty(cls, n_pages: int, page_size: int, n_kv: int, head_dim: int, page_table, seq_len,
@@ -749,15 +764,15 @@ def rope_frequencies(theta: float, rotary_dim: int, device="cuda") -> torch.Tens
     return (float(theta) ** (-2.0 * i / rotary_dim)).to(device)
 
 
-def _rows(t, B: int, n_max: int, width: int, name: str):
-    """Pointer and row stride of [B, n_max, width] F32 rows that may be part of wider ones."""
-    if t is None:
-        return None, 0
-    if not t.is_cuda or t.dtype != F32 or tuple(t.shape) != (B, n_max, width):
-        raise TypeError(f"{name}: expected a CUDA {F32} tensor [{B}, {n_max}, {width}], got "
-                        f"{t.dtype} {list(t.shape)} on {t.device}")
-    ld = t.stride(1) if n_max > 1 else (t.stride(0) if B > 1 else max(t.stride(1), width))
-    if (width > 1 and t.stride(2) != 1) or (B > 1 and t.stride(0) != n_max * ld):
+def _rows(t, dev: int, shape, name: str):
+    """Address and row stride of F32 rows [B, n, width] that may be part of wider ones."""
+    if t.dtype is not F32 or t.get_device() != dev or t.shape != shape:
+        raise _misfit(t, F32, dev, shape, name)
+    B, n, width = shape
+    sb, ld, one = t.stride()
+    if n == 1:
+        ld = sb if B > 1 else max(ld, width)
+    if one != 1 or (B > 1 and sb != n * ld):
         raise TypeError(f"{name}: rows must be evenly spaced with unit stride inside, got strides "
                         f"{t.stride()}")
     return t.data_ptr(), ld
@@ -770,56 +785,46 @@ def kv_append_paged(cache: PagedKv, q, k, v, q_out=None, n_new=None, q_norm=None
     None, k and v [B, n, n_kv * d] (each may be a slice of one projection's rows); q_out
     [B, n, nq, d]; n_new [B] int32 or None; inv_freq [rot / 2] float64 or None (no rotation);
     positions [axes, B, n] int32 or None; axis [rot / 2] uint8 or None."""
-    B, n_max = k.shape[0], k.shape[1]
-    d = cache.head_dim
-    if B != cache.batch:
-        raise ValueError(f"k has {B} sequences, the cache {cache.batch}")
-    nq = 0 if q is None else q.shape[2] // d
-    qp, ldq = _rows(q, B, n_max, nq * d, "q")
-    kp, ldk = _rows(k, B, n_max, cache.n_kv * d, "k")
-    vp, ldv = _rows(v, B, n_max, cache.n_kv * d, "v")
-    if (q is None) != (q_out is None) or (q is not None and tuple(q_out.shape) != (B, n_max, nq, d)):
-        raise ValueError(f"q_out must be [{B}, {n_max}, {nq}, {d}] with q, None without")
-    _sizes("kv_append_paged", (n_new, (B,)), (q_norm, (d,)), (k_norm, (d,)))
+    dev, B, d = cache.dev, cache.batch, cache.head_dim
+    n = k.shape[1]
+    kp, ldk = _rows(k, dev, (B, n, cache.n_kv * d), "k")
+    vp, ldv = _rows(v, dev, (B, n, cache.n_kv * d), "v")
+    nq = qp = ldq = 0
+    if q is not None:
+        nq = q.shape[2] // d
+        qp, ldq = _rows(q, dev, (B, n, nq * d), "q")
+        if q_out is None:
+            raise ValueError("q needs q_out")
     rope = None
     if inv_freq is not None:
         half = inv_freq.shape[0]
         axes = 1 if positions is None else positions.shape[0]
-        _sizes("kv_append_paged", (positions, (axes, B, n_max)), (axis, (half,)))
-        rope = ctypes.byref(RopeC(_dev(inv_freq, F64, "inv_freq"), _dev(positions, I32, "positions"),
-                                  _dev(axis, U8, "axis"), 2 * half, axes))
+        rope = ctypes.byref(RopeC(_arg(inv_freq, F64, dev, (half,), "inv_freq"),
+                                  _arg(positions, I32, dev, (axes, B, n), "positions"),
+                                  _arg(axis, U8, dev, (half,), "axis"), 2 * half, axes))
     elif positions is not None or axis is not None:
         raise ValueError("positions and axis need inv_freq")
-    _same_device(cache, q, k, v, q_out, n_new, q_norm, k_norm, inv_freq, positions, axis, d_status)
-    _run(cache.device, stream, lib().df_kv_append_paged, cache.ref, qp, ldq, nq, kp, ldk, vp, ldv,
-         _dev(q_norm, F32, "q_norm"), _dev(k_norm, F32, "k_norm"), eps, rope,
-         _dev(n_new, I32, "n_new"), n_max, _dev(q_out, F32, "q_out"), _dev(d_status, I32, "d_status"))
-
-
-def _sizes(call: str, *pairs):
-    for t, shape in pairs:
-        if t is not None and tuple(t.shape) != shape:
-            raise ValueError(f"{call}: expected {list(shape)}, got {list(t.shape)}")
+    _launch(dev, stream, lib().df_kv_append_paged, cache.ref, qp or None, ldq, nq, kp, ldk, vp, ldv,
+            _arg(q_norm, F32, dev, (d,), "q_norm"), _arg(k_norm, F32, dev, (d,), "k_norm"), eps,
+            rope, _arg(n_new, I32, dev, (B,), "n_new"), n,
+            _arg(q_out, F32, dev, (B, n, nq, d), "q_out"), _arg(d_status, I32, dev, (1,), "d_status"))
 
 
 def kv_gather_paged(cache: PagedKv, n, k_out, v_out, start=None, d_status=None, stream=None):
     """Cached rows start[b] .. start[b] + n[b] as F32 values (df_kv_gather_paged): k_out, v_out
     [B, n_kv, n_max, d], the layout df_attention reads; n and start [B] int32 or None."""
-    B, n_max = cache.batch, k_out.shape[2]
+    dev, B, n_max = cache.dev, cache.batch, k_out.shape[2]
     shape = (B, cache.n_kv, n_max, cache.head_dim)
-    _sizes("kv_gather_paged", (k_out, shape), (v_out, shape), (n, (B,)), (start, (B,)))
-    _same_device(cache, n, k_out, v_out, start, d_status)
-    _run(cache.device, stream, lib().df_kv_gather_paged, cache.ref, _dev(start, I32, "start"),
-         _dev(n, I32, "n"), n_max, _dev(k_out, F32, "k_out"), _dev(v_out, F32, "v_out"),
-         _dev(d_status, I32, "d_status"))
+    _launch(dev, stream, lib().df_kv_gather_paged, cache.ref, _arg(start, I32, dev, (B,), "start"),
+            _arg(n, I32, dev, (B,), "n"), n_max, _arg(k_out, F32, dev, shape, "k_out"),
+            _arg(v_out, F32, dev, shape, "v_out"), _arg(d_status, I32, dev, (1,), "d_status"))
 
 
 def kv_advance(seq_len, n, cap: int, d_status=None, stream=None):
     """seq_len[b] += n[b], at most cap: after the rows of a step have been appended."""
-    _sizes("kv_advance", (n, tuple(seq_len.shape)))
-    _same_device(seq_len, n, d_status)
-    _run(seq_len.device, stream, lib().kv_advance, _dev(seq_len, I32, "seq_len"), _dev(n, I32, "n"),
-         seq_len.shape[0], cap, _dev(d_status, I32, "d_status"))
+    dev, B = seq_len.get_device(), seq_len.shape[0]
+    _launch(dev, stream, lib().kv_advance, _arg(seq_len, I32, max(dev, 0), (B,), "seq_len"),
+            _arg(n, I32, dev, (B,), "n"), B, cap, _arg(d_status, I32, dev, (1,), "d_status"))
 
 
 def attention_paged_workspace_bytes(cache: PagedKv, blk: int, nq: int) -> int:
@@ -831,15 +836,14 @@ def attention_paged(cache: PagedKv, q, out, ws, n_new=None, causal: bool = False
     """Attention over the paged 4-bit cache (df_attention_paged): q and out [B, blk, nq, d];
     n_new [B] int32: row i < n_new[b] is the query of cache row seq_len[b] + i; None: blk rows over
     the seq_len[b] cached ones."""
-    B, blk, nq, d = q.shape
-    if B != cache.batch or d != cache.head_dim:
-        raise ValueError(f"q is {list(q.shape)}, the cache has {cache.batch} sequences and "
-                         f"head_dim {cache.head_dim}")
-    _sizes("attention_paged", (out, (B, blk, nq, d)), (n_new, (B,)))
-    _same_device(cache, q, out, ws, n_new, d_status)
-    _run(cache.device, stream, lib().df_attention_paged, cache.ref, _dev(q, F32, "q"),
-         _dev(n_new, I32, "n_new"), blk, nq, 1 if causal else 0, _dev(out, F32, "out"),
-         _dev(ws, U8, "ws"), ws.numel(), _dev(d_status, I32, "d_status"))
+    dev = cache.dev
+    _, blk, nq, _ = q.shape
+    shape = (cache.batch, blk, nq, cache.head_dim)
+    nb = ws.numel()
+    _launch(dev, stream, lib().df_attention_paged, cache.ref, _arg(q, F32, dev, shape, "q"),
+            _arg(n_new, I32, dev, (cache.batch,), "n_new"), blk, nq, 1 if causal else 0,
+            _arg(out, F32, dev, shape, "out"), _arg(ws, U8, dev, (nb,), "ws"), nb,
+            _arg(d_status, I32, dev, (1,), "d_status"))
 
 
 # ----------------------------------------------------------------------------- log probabilities
@@ -853,19 +857,19 @@ def token_logprobs(logits, tokens, logprob, entropy=None, top_ids=None, top_logp
     logits [R, V] (F32 or BF16; rows may be part of wider ones) at a temperature
     (df_token_logprobs). top_ids / top_logprobs [R, top_k], or both None."""
     R, V = logits.shape
-    if not logits.is_cuda or logits.dtype not in (F32, BF16) or (V > 1 and logits.stride(1) != 1):
+    dev = logits.get_device()
+    bf16 = logits.dtype is BF16
+    ld, one = logits.stride()
+    if dev < 0 or not (bf16 or logits.dtype is F32) or (V > 1 and one != 1):
         raise TypeError(f"logits: expected CUDA {F32} or {BF16} rows with unit stride, got "
                         f"{logits.dtype} {logits.stride()} on {logits.device}")
-    ld = max(logits.stride(0), V) if R == 1 else logits.stride(0)
     top_k = 0 if top_ids is None else top_ids.shape[1]
-    _sizes("token_logprobs", (tokens, (R,)), (logprob, (R,)), (entropy, (R,)), (top_ids, (R, top_k)),
-           (top_logprobs, (R, top_k)))
     if (top_ids is None) != (top_logprobs is None):
         raise ValueError("top_ids and top_logprobs go together")
-    _same_device(logits, tokens, logprob, entropy, top_ids, top_logprobs, ws, d_status)
-    _run(logits.device, stream, lib().df_token_logprobs, logits.data_ptr(),
-         1 if logits.dtype == BF16 else 0, R, V, ld, temperature, _dev(tokens, I32, "tokens"),
-         _dev(logprob, F32, "logprob"), _dev(entropy, F32, "entropy"), top_k,
-         _dev(top_ids, I32, "top_ids") if top_k else None,
-         _dev(top_logprobs, F32, "top_logprobs") if top_k else None, _dev(ws, U8, "ws"),
-         0 if ws is None else ws.numel(), _dev(d_status, I32, "d_status"))
+    nb = 0 if ws is None else ws.numel()
+    _launch(dev, stream, lib().df_token_logprobs, logits.data_ptr(), 1 if bf16 else 0, R, V,
+            V if R == 1 else ld, temperature, _arg(tokens, I32, dev, (R,), "tokens"),
+            _arg(logprob, F32, dev, (R,), "logprob"), _arg(entropy, F32, dev, (R,), "entropy"), top_k,
+            _arg(top_ids, I32, dev, (R, top_k), "top_ids") if top_k else None,
+            _arg(top_logprobs, F32, dev, (R, top_k), "top_logprobs") if top_k else None,
+            _arg(ws, U8, dev, (nb,), "ws"), nb, _arg(d_status, I32, dev, (1,), "d_status"))
