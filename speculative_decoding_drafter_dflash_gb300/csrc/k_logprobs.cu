@@ -140,6 +140,12 @@ __device__ __forceinline__ Raw<BF16> load(const uint8_t *base, int j, int mis, i
     constexpr int E = BF16 ? 8 : 4, N = BF16 ? 2 : 4, SZ = BF16 ? 2 : 4;
     const int lane = threadIdx.x & 31;
     Raw<BF16> r;
+    if (j >= mis && j + kStep <= end) {     // (most steps: no test a vector)
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            r.q[n] = *reinterpret_cast<const uint4 *>(base + (long long)(j + (n * 32 + lane) * E) * SZ);
+        return r;
+    }
 #pragma unroll
     for (int n = 0; n < N; ++n) {
         const int at = j + (n * 32 + lane) * E;
@@ -335,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const __gri
         const float bm = fmaxf(fmaxf(gm[0], gm[1]), fmaxf(gm[2], gm[3]));
         const bool want = (it == 0 ? bm >= tau0 : bm > tau) || (bm - st.mu) * c > 60.f;
         if (__any_sync(0xffffffffu, want)) {
-            follow(warp_max(bm));
+            if (__any_sync(0xffffffffu, st.mu == -INFINITY || (bm - st.mu) * c > 60.f)) follow(warp_max(bm));
             // What a held entry leaves in the step: nothing in the sums.
             const float at0 = st.mu == -INFINITY ? 0.f : st.mu, out = at0 - fmaxf(1000.f / c, fabsf(at0));
 #pragma unroll
@@ -442,6 +448,15 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const __gri
         s.U = warp_sum(s.U);
     };
 
+    // The token's own logit, on its way while the lists are joined.
+    int tk = -1;
+    float tx = 0.f;
+    auto fetch = [&]() {
+        tk = a.tokens[r];
+        if (tk >= 0 && tk < a.V)
+            tx = BF16 ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(row)[tk] << 16)
+                      : reinterpret_cast<const float *>(row)[tk];
+    };
     if (n_chunks > 1) {
         Part *parts = static_cast<Part *>(a.part) + (size_t)r * n_chunks;
         if (warp == 0) {
@@ -458,6 +473,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const __gri
         __syncthreads();
         if (!last) return;
         __threadfence();
+        fetch();
         if (threadIdx.x == 0) a.counters[r] = 0;
         M = -INFINITY;
         for (int k = lane; k < n_chunks; k += 32) M = fmaxf(M, __ldcg(&parts[k].v[0]));
@@ -496,6 +512,8 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const __gri
         st.S = warp_sum(st.S);
         st.U = warp_sum(st.U);
         join(st);
+    } else {
+        fetch();
     }
     if (warp != 0) return;
 
@@ -511,13 +529,10 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const __gri
         a.top_lp[(size_t)r * a.top_k + lane] = bad ? nan : (st.lv - M) / a.T - ls;
     }
     if (lane == 0) {
-        const int tk = a.tokens[r];
         float lp = 0.f;
         bool err = bad;
         if (tk >= 0 && tk < a.V) {
-            const float x = BF16 ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(row)[tk] << 16)
-                                 : reinterpret_cast<const float *>(row)[tk];
-            lp = (x - M) / a.T - ls;
+            lp = (tx - M) / a.T - ls;
         } else if (tk != -1) {
             lp = nan;
             err = true;
