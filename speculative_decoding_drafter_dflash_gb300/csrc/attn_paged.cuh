@@ -196,62 +196,91 @@ __device__ __forceinline__ float *part_of(const AttnPagedArgs &a, int first, int
 }
 
 // The last of a task's CTAs joins the partial results. THREADS threads (tid from 0), sync() their
-// barrier; fac: shared [CTAs of the task][RT], sum: shared [RT], flag: shared; DEPTH parts are loaded
-// together.
-template <int D, int RT, int THREADS, int DEPTH, class Sync>
+// barrier; fac: shared [CTAs of the task][RT], sum: shared [RT], flag: shared. It is a chain of
+// latencies of the L2 that other CTAs no longer hide, so what can be asked for at once is: DEPTH parts
+// of WIDE places a thread, before the factors that they wait for.
+template <int D, int RT, int THREADS, int WIDE, int DEPTH, class Sync>
 __device__ void join_parts(const AttnPagedArgs &a, const Piece &p, int tid, Sync sync, float *fac, float *sum,
                            int *flag) {
+    constexpr int W = THREADS / 32, ROWS = (RT + W - 1) / W;
     const int lane = tid & 31, warp = tid >> 5, cnt = p.last - p.first + 1;
-    __threadfence();
     sync();
-    if (tid == 0) *flag = atomicAdd(a.counters + p.first, 1) == cnt - 1;
+    if (tid == 0) {
+        const bool all = count_in(a.counters + p.first) == cnt - 1;
+        if (all) a.counters[p.first] = 0;
+        *flag = all;
+    }
     sync();
     if (!*flag) return;
-    __threadfence();
-    if (tid == 0) a.counters[p.first] = 0;
-    for (int rr = warp; rr < p.nr; rr += THREADS / 32) {
-        float mx = -INFINITY;
-        for (int k = lane; k < cnt; k += 32)
-            mx = fmaxf(mx, __ldcg(part_of<D, RT>(a, p.first, p.first + k) + RT * D + 2 * rr));
+    // (the first CTA's part is in its second place, the others' in their first)
+    auto at = [&](int k) { return part_of<D, RT>(a, p.first, p.first + k); };
+    auto stat = [&](int k, int rr) { return __ldcg(reinterpret_cast<const float2 *>(at(k) + RT * D) + rr); };
+    const int places = p.nr * (D / 4);
+    float4 v[WIDE][DEPTH];
+    auto ask = [&](int f0, int k0) {
+#pragma unroll
+        for (int w = 0; w < WIDE; ++w) {
+            const int f = f0 + w * THREADS;
+#pragma unroll
+            for (int k = 0; k < DEPTH; ++k)
+                if (f < places && k0 + k < cnt) v[w][k] = __ldcg(reinterpret_cast<const float4 *>(at(k0 + k)) + f);
+        }
+    };
+    float2 st[ROWS];                         // a warp's rows, 32 parts
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {
+        const int rr = warp + j * W;
+        st[j] = rr < p.nr && lane < cnt ? stat(lane, rr) : make_float2(-INFINITY, 0.f);
+    }
+    ask(tid, 0);
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {
+        const int rr = warp + j * W;
+        if (rr >= p.nr) continue;
+        float mx = st[j].x;
+        for (int k = lane + 32; k < cnt; k += 32) mx = fmaxf(mx, stat(k, rr).x);
         mx = warp_max(mx);
         float s = 0.f;
         for (int k = lane; k < cnt; k += 32) {
-            const float2 v = __ldcg(reinterpret_cast<const float2 *>(part_of<D, RT>(a, p.first, p.first + k) + RT * D) + rr);
+            const float2 t = k < 32 ? st[j] : stat(k, rr);
             // (a part without a visible key counts 0, unless its sum is a NaN row's NaN)
-            const float f = v.x == -INFINITY ? (v.y == v.y ? 0.f : v.y) : exp2f(v.x - mx);
+            const float f = t.x == -INFINITY ? (t.y == t.y ? 0.f : t.y) : exp2f(t.x - mx);
             fac[k * RT + rr] = f;
-            s += v.x == -INFINITY ? v.y : v.y * f;
+            s += t.x == -INFINITY ? t.y : t.y * f;
         }
         s = warp_sum(s);
         if (lane == 0) sum[rr] = s;
     }
     sync();
-    for (int f = tid; f < p.nr * (D / 4); f += THREADS) {
-        const int rr = f / (D / 4), dim = 4 * (f - rr * (D / 4));
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        // (the first CTA's part is in its second place, the others' in their first)
-        const float *at = part_of<D, RT>(a, p.first, p.first) + rr * D + dim;
-        const float *next = part_of<D, RT>(a, p.first, p.first + 1) + rr * D + dim;
+    for (int f0 = tid; f0 < places; f0 += WIDE * THREADS) {
+        float4 acc[WIDE];
+#pragma unroll
+        for (int w = 0; w < WIDE; ++w) acc[w] = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int k0 = 0; k0 < cnt; k0 += DEPTH) {
-            float4 v[DEPTH];
+            if (f0 != tid || k0 > 0) ask(f0, k0);
 #pragma unroll
-            for (int k = 0; k < DEPTH; ++k)
-                if (k0 + k < cnt)
-                    v[k] = __ldcg(reinterpret_cast<const float4 *>(
-                        k0 + k == 0 ? at : next + (size_t)(k0 + k - 1) * 2 * RT * (D + 2)));
+            for (int w = 0; w < WIDE; ++w) {
+                const int f = f0 + w * THREADS;
+                if (f >= places) break;
 #pragma unroll
-            for (int k = 0; k < DEPTH; ++k) {
-                if (k0 + k >= cnt) break;
-                const float w = fac[(k0 + k) * RT + rr];
-                acc.x = fmaf(v[k].x, w, acc.x);
-                acc.y = fmaf(v[k].y, w, acc.y);
-                acc.z = fmaf(v[k].z, w, acc.z);
-                acc.w = fmaf(v[k].w, w, acc.w);
+                for (int k = 0; k < DEPTH; ++k) {
+                    if (k0 + k >= cnt) break;
+                    const float x = fac[(k0 + k) * RT + f / (D / 4)];
+                    acc[w].x = fmaf(v[w][k].x, x, acc[w].x);
+                    acc[w].y = fmaf(v[w][k].y, x, acc[w].y);
+                    acc[w].z = fmaf(v[w][k].z, x, acc[w].z);
+                    acc[w].w = fmaf(v[w][k].w, x, acc[w].w);
+                }
             }
         }
-        const float inv = sum[rr] == 0.f ? 0.f : a.c.v_scale / sum[rr];
-        *reinterpret_cast<float4 *>(a.out + row_offset(a, p, rr) + dim) =
-            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+#pragma unroll
+        for (int w = 0; w < WIDE; ++w) {
+            const int f = f0 + w * THREADS, rr = f / (D / 4);
+            if (f >= places) break;
+            const float inv = sum[rr] == 0.f ? 0.f : a.c.v_scale / sum[rr];
+            *reinterpret_cast<float4 *>(a.out + row_offset(a, p, rr) + 4 * (f % (D / 4))) =
+                make_float4(acc[w].x * inv, acc[w].y * inv, acc[w].z * inv, acc[w].w * inv);
+        }
     }
 }
 

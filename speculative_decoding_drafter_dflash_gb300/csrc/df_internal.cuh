@@ -111,6 +111,15 @@ __device__ __forceinline__ void set_status(int32_t *st, int code) {
     if (st) atomicCAS(st, 0, code);
 }
 
+// Arrival at a counter, one thread after a barrier: its CTA's (warp's) writes before it are seen by
+// those after the barrier that follows the last arrival. (One fence, where a fence of every
+// thread costs a small kernel half a microsecond.)
+__device__ __forceinline__ int count_in(int *counter) {
+    int was;
+    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(was) : "l"(counter) : "memory");
+    return was;
+}
+
 // Trace builds (build.py --trace: -DDF_TRACE=1 with relocatable device code, a separate
 // libdflash_trace.so): every kernel's CTAs record (kernel id, SM, start, end) in nanoseconds of
 // the global timer into one device buffer, read back by df_trace_read; the launches of a CUDA

@@ -106,70 +106,19 @@ __global__ void __launch_bounds__(32 * kWarps, D * NT <= 128 ? 2 : 1)
         const Piece p = next_piece<kUnit, RT, kExtra>(a, line, off, u, u_end);
         const int x0 = p.x0, x1 = p.x1, nr = p.nr;
 
-        // Query rows as B fragments: [k step][row tile][lane] = (hi, hi, lo, lo) of four
-        // consecutive dims, which are the four that the thread's K fragment holds.
-        for (int rr = warp; rr < RT; rr += kWarps) {
-            constexpr int GR = D / 4, PER = (GR + 31) / 32;
-            const float unit = kLog2e / sqrtf((float)D);
-            float4 v[PER];
-            float amax = 0.f;
-#pragma unroll
-            for (int k = 0; k < PER; ++k) {
-                const int gi = lane + 32 * k;
-                v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (rr < nr && gi < GR)
-                    v[k] = *reinterpret_cast<const float4 *>(a.q + row_offset(a, p, rr) + 4 * gi);
-                // log2(e) / sqrt(d) is taken into q, so that a row's scale is a power of two
-                v[k].x *= unit;
-                v[k].y *= unit;
-                v[k].z *= unit;
-                v[k].w *= unit;
-                amax = fmaxf(fmaxf(amax, fmaxf(fabsf(v[k].x), fabsf(v[k].y))),
-                             fmaxf(fabsf(v[k].z), fabsf(v[k].w)));
-            }
-            amax = warp_max(amax);
-            float down, up;
-            row_scale(amax, down, up);
-#pragma unroll
-            for (int k = 0; k < PER; ++k) {
-                const int gi = lane + 32 * k;
-                if (gi >= GR) continue;
-                const float x0f = v[k].x * down, x1f = v[k].y * down, x2f = v[k].z * down, x3f = v[k].w * down;
-                uint4 f;
-                split_f16(x0f, x1f, f.x, f.z);
-                split_f16(x2f, x3f, f.y, f.w);
-                int tt, j;
-                if constexpr (D == 64) tt = gi >> 2, j = gi & 3;
-                else tt = (gi & 31) >> 3, j = (gi >> 5) * 8 + (gi & 7);
-                qf[(j * NT + (rr >> 3)) * 32 + (rr & 7) * 4 + tt] = f;
-            }
-            if (lane == 0) {
-                rscale[rr] = a.c.k_scale * up;
-                rlim[rr] = rr < nr ? row_limit(a, p, rr) : 0;
-            }
-        }
-        __syncthreads();
-
-        float rs[NT][2];
-        int lim_min = 0x7fffffff;
-        for (int rr = 0; rr < nr; ++rr) lim_min = min(lim_min, rlim[rr]);
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                rs[n][e] = rscale[n * 8 + 2 * t + e];
-            }
-        float o[MT][NT][4], m[NT][2], l[NT][2];
+        // The query rows, the pages and the first steps are on their way together.
+        constexpr int GR = D / 4, PER = (GR + 31) / 32;
+        float4 qv[NT][PER];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            m[n][0] = m[n][1] = kLowest;
-            l[n][0] = l[n][1] = 0.f;
+            const int rr = warp + n * kWarps;
+            const float *src = a.q + (rr < nr ? row_offset(a, p, rr) : 0);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.f;
+            for (int k = 0; k < PER; ++k) {
+                qv[n][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (rr < nr && lane + 32 * k < GR) qv[n][k] = *reinterpret_cast<const float4 *>(src + 4 * (lane + 32 * k));
+            }
         }
-
         uint8_t *my = ring + warp * kStages * L::kStage;
         const int32_t *table = a.c.page_table + (size_t)p.b * a.c.max_pages;
         // A step is two groups of 16 rows, each within a page: D / 2 chunks of 16 bytes of K and of V
@@ -220,6 +169,75 @@ __global__ void __launch_bounds__(32 * kWarps, D * NT <= 128 ? 2 : 1)
             }
         };
 
+        int pg[2];
+        {
+            int first[kStages][2];
+#pragma unroll
+            for (int s = 0; s < kStages; ++s) pages_of(x0 + warp + s * kWarps, first[s]);
+            pages_of(x0 + warp + kStages * kWarps, pg);
+#pragma unroll
+            for (int s = 0; s < kStages; ++s) {
+                issue(x0 + warp + s * kWarps, s, first[s]);
+                cp_commit();
+            }
+        }
+        // Query rows as B fragments: [k step][row tile][lane] = (hi, hi, lo, lo) of four
+        // consecutive dims, which are the four that the thread's K fragment holds.
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int rr = warp + n * kWarps;
+            float amax = 0.f;
+#pragma unroll
+            for (int k = 0; k < PER; ++k) {
+                float4 &v = qv[n][k];
+                // log2(e) / sqrt(d) is taken into q, so that a row's scale is a power of two
+                const float unit = kLog2e / sqrtf((float)D);
+                v = make_float4(v.x * unit, v.y * unit, v.z * unit, v.w * unit);
+                amax = fmaxf(fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
+            }
+            amax = warp_max(amax);
+            float down, up;
+            row_scale(amax, down, up);
+#pragma unroll
+            for (int k = 0; k < PER; ++k) {
+                const int gi = lane + 32 * k;
+                if (gi >= GR) continue;
+                const float4 v = qv[n][k];
+                uint4 f;
+                split_f16(v.x * down, v.y * down, f.x, f.z);
+                split_f16(v.z * down, v.w * down, f.y, f.w);
+                int tt, j;
+                if constexpr (D == 64) tt = gi >> 2, j = gi & 3;
+                else tt = (gi & 31) >> 3, j = (gi >> 5) * 8 + (gi & 7);
+                qf[(j * NT + (rr >> 3)) * 32 + (rr & 7) * 4 + tt] = f;
+            }
+            if (lane == 0) {
+                rscale[rr] = a.c.k_scale * up;
+                rlim[rr] = rr < nr ? row_limit(a, p, rr) : 0;
+            }
+        }
+        __syncthreads();
+
+        float rs[NT][2];
+        int lim_min = 0x7fffffff;
+        for (int rr = 0; rr < nr; ++rr) lim_min = min(lim_min, rlim[rr]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                rs[n][e] = rscale[n * 8 + 2 * t + e];
+            }
+        float o[MT][NT][4], m[NT][2], l[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            m[n][0] = m[n][1] = kLowest;
+            l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.f;
+        }
+
         // The tensor core's F32 accumulation rounds towards zero, so a long run of products would
         // drift: every kFlush steps the outputs join sums in shared memory, rounded to nearest.
         float4 *mine = sums + warp * MT * NT * 32 + lane;
@@ -239,14 +257,6 @@ __global__ void __launch_bounds__(32 * kWarps, D * NT <= 128 ? 2 : 1)
             steps = 0;
         };
 
-        int pg[2];
-#pragma unroll
-        for (int s = 0; s < kStages; ++s) {
-            pages_of(x0 + warp + s * kWarps, pg);
-            issue(x0 + warp + s * kWarps, s, pg);
-            cp_commit();
-        }
-        pages_of(x0 + warp + kStages * kWarps, pg);
         int stage = 0;
         for (int x = x0 + warp; x < x1; x += kWarps) {
             cp_wait<kStages - 1>();
@@ -528,8 +538,8 @@ __global__ void __launch_bounds__(32 * kWarps, D * NT <= 128 ? 2 : 1)
                 part[RT * D + 2 * tid] = rm[tid];
                 part[RT * D + 2 * tid + 1] = rl[tid];
             }
-            join_parts<D, RT, 32 * kWarps, (D == 256 ? 16 : 8)>(a, p, tid, [] { __syncthreads(); }, reinterpret_cast<float *>(ring),
-                                           reinterpret_cast<float *>(ml), misc + 32);
+            join_parts<D, RT, 32 * kWarps, D * NT <= 128 ? 1 : 2, D * NT <= 128 ? 8 : 12>(
+                a, p, tid, [] { __syncthreads(); }, reinterpret_cast<float *>(ring), reinterpret_cast<float *>(ml), misc + 32);
         }
         __syncthreads();
     }

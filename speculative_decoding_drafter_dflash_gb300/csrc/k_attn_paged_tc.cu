@@ -751,7 +751,7 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1) attn_paged_tc_kernel(
                 }
                 // The factors of the join (one a CTA of the task and row) take the P buffers:
                 // every P V has completed.
-                join_parts<D, NP, 32 * kSoftWarps, 4>(a, p, st_id, all_sync, reinterpret_cast<float *>(pbuf), red, flag);
+                join_parts<D, NP, 32 * kSoftWarps, 1, 4>(a, p, st_id, all_sync, reinterpret_cast<float *>(pbuf), red, flag);
             }
             all_sync();
             if (lane == 0) mbar_arrive(&q_free[qb]);

@@ -466,15 +466,15 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const __gri
                 parts[ck].S = st.S;
                 parts[ck].U = st.U;
             }
-            __threadfence();
             __syncwarp();
-            if (lane == 0) last = atomicAdd(a.counters + r, 1) == n_chunks - 1;
+            if (lane == 0) {
+                last = count_in(a.counters + r) == n_chunks - 1;
+                if (last) a.counters[r] = 0;
+            }
         }
         __syncthreads();
         if (!last) return;
-        __threadfence();
         fetch();
-        if (threadIdx.x == 0) a.counters[r] = 0;
         M = -INFINITY;
         for (int k = lane; k < n_chunks; k += 32) M = fmaxf(M, __ldcg(&parts[k].v[0]));
         M = warp_max(M);
