@@ -7,7 +7,8 @@
 // are the 8-wide columns. A cached value c * s has 2 + 4 significant bits, so it is an FP16
 // value exactly (one conversion and one packed multiply for two values); q (scaled by a power of
 // two to at most 1 a row) and the probabilities enter as FP16 pairs hi + lo, about 22 bits, so a
-// product carries F32's accuracy for two matrix instructions.
+// product carries F32's accuracy for two matrix instructions. Up to 4 rows the pairs lie side by
+// side instead, hi in columns 0 to 3 and lo in 4 to 7, and one instruction takes both.
 #include "attn_paged.cuh"
 
 namespace df {
@@ -75,12 +76,13 @@ constexpr size_t paged_smem(int batch) {
            (size_t)kWarps * 8 * NT * 8 + 8 * NT * 16 + 64 * 4 + (size_t)(batch + 1) * 4;
 }
 
-template <int D, int NT>
+// 8 NT query rows a task, or 4 (PAIRS: a row's hi and lo are columns of their own).
+template <int D, int NT, bool PAIRS>
 __global__ void __launch_bounds__(32 * kWarps, D * NT <= 128 ? 2 : 1)
     attn_paged_kernel(const __grid_constant__ AttnPagedArgs a) {
     DF_TRACE_KERNEL(TK_ATTN_PAGED);
     using L = Lay<D>;
-    constexpr int RT = 8 * NT, KS = D / 16, MT = D / 16;
+    constexpr int RT = PAIRS ? 4 : 8 * NT, KS = D / 16, MT = D / 16;
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t *ring = smem;
     float4 *sums = reinterpret_cast<float4 *>(ring + kWarps * kStages * L::kStage);   // [kWarps][MT * NT][32]
@@ -94,6 +96,7 @@ __global__ void __launch_bounds__(32 * kWarps, D * NT <= 128 ? 2 : 1)
     int *off = misc + 64;                                                         // [batch + 1]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
+    const int col = PAIRS ? 2 * (t & 1) : 2 * t;                                  // row of the thread's first column
     const int nkv = a.c.n_kv_heads;
     const int pshift = 31 - __clz(a.c.page_size);
     pdl_trigger();
@@ -186,6 +189,7 @@ __global__ void __launch_bounds__(32 * kWarps, D * NT <= 128 ? 2 : 1)
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int rr = warp + n * kWarps;
+            if (rr >= RT) break;
             float amax = 0.f;
 #pragma unroll
             for (int k = 0; k < PER; ++k) {
@@ -209,7 +213,13 @@ __global__ void __launch_bounds__(32 * kWarps, D * NT <= 128 ? 2 : 1)
                 int tt, j;
                 if constexpr (D == 64) tt = gi >> 2, j = gi & 3;
                 else tt = (gi & 31) >> 3, j = (gi >> 5) * 8 + (gi & 7);
-                qf[(j * NT + (rr >> 3)) * 32 + (rr & 7) * 4 + tt] = f;
+                if constexpr (PAIRS) {
+                    uint2 *to = reinterpret_cast<uint2 *>(qf) + j * 32 + rr * 4 + tt;
+                    to[0] = make_uint2(f.x, f.y);
+                    to[16] = make_uint2(f.z, f.w);
+                } else {
+                    qf[(j * NT + (rr >> 3)) * 32 + (rr & 7) * 4 + tt] = f;
+                }
             }
             if (lane == 0) {
                 rscale[rr] = a.c.k_scale * up;
@@ -225,7 +235,7 @@ __global__ void __launch_bounds__(32 * kWarps, D * NT <= 128 ? 2 : 1)
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                rs[n][e] = rscale[n * 8 + 2 * t + e];
+                rs[n][e] = rscale[n * 8 + col + e];
             }
         float o[MT][NT][4], m[NT][2], l[NT][2];
 #pragma unroll
@@ -314,17 +324,30 @@ __global__ void __launch_bounds__(32 * kWarps, D * NT <= 128 ? 2 : 1)
                         const int j = c * 8 + 2 * w + jj;
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            const uint4 f = qf[(j * NT + n) * 32 + lane];
+                            uint4 f = make_uint4(0, 0, 0, 0);
+                            if constexpr (PAIRS) {
+                                const uint2 h = reinterpret_cast<const uint2 *>(qf)[j * 32 + lane];
+                                f.x = h.x, f.y = h.y;
+                            } else {
+                                f = qf[(j * NT + n) * 32 + lane];
+                            }
 #pragma unroll
                             for (int sb = 0; sb < 2; ++sb) {
                                 mma16816(s[sb][n], k0[sb][2 * jj], k1[sb][2 * jj], k0[sb][2 * jj + 1],
                                          k1[sb][2 * jj + 1], f.x, f.y);
-                                mma16816(s[sb][n], k0[sb][2 * jj], k1[sb][2 * jj], k0[sb][2 * jj + 1],
-                                         k1[sb][2 * jj + 1], f.z, f.w);
+                                if constexpr (!PAIRS)
+                                    mma16816(s[sb][n], k0[sb][2 * jj], k1[sb][2 * jj], k0[sb][2 * jj + 1],
+                                             k1[sb][2 * jj + 1], f.z, f.w);
                             }
                         }
                     }
                 }
+            }
+            if constexpr (PAIRS) {           // hi + lo (both columns' threads go on with the sum)
+#pragma unroll
+                for (int sb = 0; sb < 2; ++sb)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[sb][0][e] += __shfl_xor_sync(0xffffffffu, s[sb][0][e], 2);
             }
             // The keys a row may not see drop out.
             const int key0 = x * kUnit;
@@ -336,7 +359,7 @@ __global__ void __launch_bounds__(32 * kWarps, D * NT <= 128 ? 2 : 1)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int key = key0 + 16 * sb + key_of(g) + 8 * (e >> 1);
-                            if (key >= rlim[n * 8 + 2 * t + (e & 1)]) s[sb][n][e] = -INFINITY;
+                            if (key >= rlim[n * 8 + col + (e & 1)]) s[sb][n][e] = -INFINITY;
                         }
             }
             // Exponents against the row's reference, in log2 units (rs is a power of two: the
@@ -394,8 +417,12 @@ __global__ void __launch_bounds__(32 * kWarps, D * NT <= 128 ? 2 : 1)
                         l[n][1] += p1;
                         uint32_t hh, ll;
                         split_f16(p0, p1, hh, ll);
-                        ph[sb][n][e] = movm(hh);
-                        pl[sb][n][e] = movm(ll);
+                        if constexpr (PAIRS) {
+                            ph[sb][n][e] = movm(t < 2 ? hh : ll);
+                        } else {
+                            ph[sb][n][e] = movm(hh);
+                            pl[sb][n][e] = movm(ll);
+                        }
                     }
             // O^T += V^T P^T: a thread holds d / 8 consecutive dims of four keys; nibbles of two
             // keys are interleaved so that one conversion gives a pair of keys.
@@ -445,7 +472,8 @@ __global__ void __launch_bounds__(32 * kWarps, D * NT <= 128 ? 2 : 1)
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             mma16816(o[4 * w + e][n], f0, f1, f2, f3, ph[sb][n][0], ph[sb][n][1]);
-                            mma16816(o[4 * w + e][n], f0, f1, f2, f3, pl[sb][n][0], pl[sb][n][1]);
+                            if constexpr (!PAIRS)
+                                mma16816(o[4 * w + e][n], f0, f1, f2, f3, pl[sb][n][0], pl[sb][n][1]);
                         }
                     }
                 }
@@ -481,7 +509,7 @@ __global__ void __launch_bounds__(32 * kWarps, D * NT <= 128 ? 2 : 1)
                 v += __shfl_xor_sync(0xffffffffu, v, 4);
                 v += __shfl_xor_sync(0xffffffffu, v, 8);
                 v += __shfl_xor_sync(0xffffffffu, v, 16);
-                if (g == 0) ml[warp * RT + n * 8 + 2 * t + e] = make_float2(m[n][e], v);
+                if (g == 0 && (!PAIRS || t < 2)) ml[warp * RT + n * 8 + 2 * t + e] = make_float2(m[n][e], v);
             }
         __syncthreads();
         float4 *ob = reinterpret_cast<float4 *>(ring);
@@ -505,13 +533,18 @@ __global__ void __launch_bounds__(32 * kWarps, D * NT <= 128 ? 2 : 1)
         __syncthreads();
         const bool whole = p.whole();
         float *part = part_of<D, RT>(a, p.first, (int)blockIdx.x);
-        for (int f = tid; f < MT * NT * 32; f += 32 * kWarps) {
-            const int ln = f & 31, tile = f >> 5, n = tile % NT, mt = tile / NT;
-            const int ra = n * 8 + 2 * (ln & 3), dim = (ln >> 2) * (D / 8) + 2 * mt;
+        constexpr int TP = PAIRS ? 2 : 4;                     // threads of different rows
+        for (int f = tid; f < MT * NT * 8 * TP; f += 32 * kWarps) {
+            const int lg = (f / TP) & 7, lt = f % TP, ln = lg * 4 + lt, tile = f / (8 * TP), n = tile % NT, mt = tile / NT;
+            const int ra = n * 8 + 2 * lt, dim = lg * (D / 8) + 2 * mt;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float4 v = ob[w * MT * NT * 32 + f];
+                float4 v = ob[w * MT * NT * 32 + tile * 32 + ln];
+                if constexpr (PAIRS) {
+                    const float4 lo = ob[w * MT * 32 + tile * 32 + ln + 2];
+                    v = make_float4(v.x + lo.x, v.y + lo.y, v.z + lo.z, v.w + lo.w);
+                }
                 const float f0 = ml[w * RT + ra].x, f1 = ml[w * RT + ra + 1].x;
                 acc.x = fmaf(v.x, f0, acc.x);
                 acc.y = fmaf(v.y, f1, acc.y);
@@ -546,22 +579,24 @@ __global__ void __launch_bounds__(32 * kWarps, D * NT <= 128 ? 2 : 1)
 }
 
 struct Plan {
+    bool pairs;
     int nt, rt, rb, ctas;
 };
 Plan plan_of(const df_paged_kv &c, int blk, int nq) {
     Plan p;
     const int rows = blk * (nq / c.n_kv_heads);
+    p.pairs = rows <= 4;
     p.nt = rows <= 8 || c.head_dim == 256 ? 1 : 2;
-    p.rt = 8 * p.nt;
+    p.rt = p.pairs ? 4 : 8 * p.nt;
     p.rb = (rows + p.rt - 1) / p.rt;
     p.ctas = sm_count() * (c.head_dim * p.nt <= 128 ? 2 : 1);
     if (p.ctas > kOpsCounters) p.ctas = kOpsCounters;
     return p;
 }
 
-template <int D, int NT>
+template <int D, int NT, bool PAIRS>
 int launch_one(const AttnPagedArgs &a, const Plan &p, cudaStream_t s) {
-    return launch_k("attn_paged_kernel", attn_paged_kernel<D, NT>, dim3(p.ctas), dim3(32 * kWarps),
+    return launch_k("attn_paged_kernel", attn_paged_kernel<D, NT, PAIRS>, dim3(p.ctas), dim3(32 * kWarps),
                     paged_smem<D, NT>(a.c.batch), s, a);
 }
 
@@ -578,12 +613,15 @@ int launch_attn_paged(const AttnPagedArgs &a, cudaStream_t s) {
     const PagedTcPlan t = attn_paged_tc_plan(a.c, a.blk, a.nq);
     if (t.np) return launch_attn_paged_tc(a, t, s);
     const Plan p = plan_of(a.c, a.blk, a.nq);
-    switch (a.c.head_dim * 4 + p.nt) {
-        case 64 * 4 + 1: return launch_one<64, 1>(a, p, s);
-        case 64 * 4 + 2: return launch_one<64, 2>(a, p, s);
-        case 128 * 4 + 1: return launch_one<128, 1>(a, p, s);
-        case 128 * 4 + 2: return launch_one<128, 2>(a, p, s);
-        default: return launch_one<256, 1>(a, p, s);
+    switch (a.c.head_dim * 4 + (p.pairs ? 0 : p.nt)) {
+        case 64 * 4: return launch_one<64, 1, true>(a, p, s);
+        case 64 * 4 + 1: return launch_one<64, 1, false>(a, p, s);
+        case 64 * 4 + 2: return launch_one<64, 2, false>(a, p, s);
+        case 128 * 4: return launch_one<128, 1, true>(a, p, s);
+        case 128 * 4 + 1: return launch_one<128, 1, false>(a, p, s);
+        case 128 * 4 + 2: return launch_one<128, 2, false>(a, p, s);
+        case 256 * 4: return launch_one<256, 1, true>(a, p, s);
+        default: return launch_one<256, 1, false>(a, p, s);
     }
 }
 
