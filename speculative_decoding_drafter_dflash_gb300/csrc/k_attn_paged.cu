@@ -9,6 +9,17 @@
 // two to at most 1 a row) and the probabilities enter as FP16 pairs hi + lo, about 22 bits, so a
 // product carries F32's accuracy for two matrix instructions. Up to 4 rows the pairs lie side by
 // side instead, hi in columns 0 to 3 and lo in 4 to 7, and one instruction takes both.
+//
+// A warp takes 32 keys a step, 8 warps a piece of a task in turn, each with a ring of its own, a
+// reference, sums and outputs; they meet at the piece's end. No warp waits for another in between.
+// Bound: for few rows the instructions that turn codes into operands (64 conversions, 64 products
+// and 48 matrix instructions a thread and step; 60% of the issue slots are taken by 16 warps an SM),
+// not the cache's bytes: 64 single tokens over up to 8191 keys each (16/8 heads of 128) 81 us, 312 MB at
+// 3.9 TB/s, with one matrix instruction for hi and lo, 91 us with two. From 5 rows on the matrix rate
+// (mma.sync gives half of it here to tcgen05): 8 x 32768 keys, 16/8 heads: 16 rows a head 122 us, 32 rows 233 us. One
+// token over 8192 keys (24/4 heads of 256) 14.2 us, a block of 16 over 4096 (16/8 of 128) 14.0 us: a
+// chain of latencies (lengths and line 1.9 us, pages, rows and first keys 2.2, a step or two 3.5, the
+// warps' join 1.5, the parts' 3.5).
 #include "attn_paged.cuh"
 
 namespace df {

@@ -18,6 +18,12 @@
 //
 // O^T accumulates in tensor memory for at most kFlush tiles of a group, then joins an F32 sum in
 // shared memory: long sums are rounded there, and a row whose maximum rises rescales there.
+//
+// 8 sequences of 32768 keys, 32 rows a head (16/8 heads of 128): 139 us, 304 MB at 2.2 TB/s and 247 TFLOP/s
+// (twice that with the lo halves; the tensor pipe is busy 21% of the time); the mma.sync kernel takes
+// 233 us.
+// What bounds it is neither: a tile is 1.3 us, of which 2/3 of the issue slots are taken, and the
+// rest is the chain from a tile's codes to its outputs, three roles long, at two tiles in flight.
 #include "attn_paged.cuh"
 #include "tc_ptx.cuh"
 
@@ -779,10 +785,10 @@ constexpr size_t kMaxSmem = 232448;
 // More than 8 query rows a head over enough keys: rows cost this kernel matrix columns and the other
 // one instructions, but a CTA's first outputs take some 10 us longer here. Measured, the other
 // kernel : this one in us, at rows a head x keys a CTA, 8 heads of K and V:
-//   D = 128   8 x 13800  87 : 114   16 x 860  26 : 26   16 x 3450  46 : 43   16 x 13800  136 : 119
-//             32 x 430   21 : 25    32 x 860  32 : 35   32 x 1725  44 : 38   32 x 13800  238 : 148
-//   D = 256   8 x 13800  143 : 188  16 x 860  33 : 37   16 x 1725  46 : 44   16 x 13800  271 : 195
-//             32 x 215   23 : 23    32 x 860  53 : 50   64 x 110   26 : 32   64 x 3450   270 : 193
+//   D = 128   8 x 13800  83 : 114   16 x 1725  27 : 29   16 x 3450  40 : 40   16 x 13800  131 : 118
+//             32 x 430   18 : 25    32 x 860   29 : 29   32 x 1725  42 : 37   32 x 13800  233 : 140
+//   D = 256   8 x 13800  141 : 192  16 x 860   30 : 32   16 x 3450  75 : 65   16 x 13800  271 : 197
+//             32 x 430   27 : 31    32 x 860   50 : 47   64 x 430   42 : 40   64 x 3450   269 : 196
 // which crosses where rows x D x keys a CTA are some 4M. Keys are counted by the page table's width,
 // which is what a launch knows of them.
 PagedTcPlan attn_paged_tc_plan(const df_paged_kv &c, int blk, int nq) {

@@ -260,7 +260,7 @@ __device__ __forceinline__ void append_rows(const KvAppendArgs &a, const AppendS
 // EPL = d / 32 consecutive dims, so a block of 16 is 16 / EPL lanes and the partner of a rotary
 // pair is the same element of another lane (rotary_dim is a multiple of 16, so half of it is one
 // of EPL). The CTA first takes the cosine and sine of its tokens' angles into shared memory,
-// where its 16 warps share them. An angle is position * inv_freq reduced to a turn: inv_freq / 2 pi
+// where its warps share them. An angle is position * inv_freq reduced to a turn: inv_freq / 2 pi
 // as a 64-bit fixed-point fraction times the position, modulo 2^64, which is exact up to the
 // fraction's own 2^-53 and takes integer multiplies instead of GB300's slow FP64; only the top
 // 32 bits of the turn enter cos and sin.
@@ -270,6 +270,11 @@ __device__ __forceinline__ void append_rows(const KvAppendArgs &a, const AppendS
 // where the two differ (about one in a thousand) are noted and taken again in float64 once the
 // CTA's rows are done (append_f64), so the codes are those of the real-number definition and the
 // float64 code takes no registers from the loop.
+//
+// 8192 rows of 16 q and 8 KV heads of 128 dims: 68 us for 211 MB, 3.1 TB/s of the copy's 6.8; 61% of
+// the issue slots are taken (150 instructions of a warp a head's row), so what is left is latency
+// between them, and spreads over waits for shared memory, for the rows and at the angles' barrier.
+// One token: 3 us. (A warp of two rows at 16 lanes each spilled and read half lines: 130 us.)
 template <int EPL>
 __global__ void __launch_bounds__(32 * kAppendWarps, EPL == 8 ? 2 : 4)
     kv_append_kernel(const __grid_constant__ KvAppendArgs a, int tokens_per_cta) {
@@ -349,7 +354,8 @@ __global__ void __launch_bounds__(32 * kAppendWarps, EPL == 8 ? 2 : 4)
 
 // Threads of a (sequence, KV head), grid y: four values each of a row, four rows at a time, so that
 // the table, the codes and the stores are each in flight four times over and a warp's stores are
-// whole lines. Bound by the F32 rows written.
+// whole lines. Bound by the F32 rows written: 8192 rows of 8 heads of 128 dims, K and V, 16 us for 77 MB,
+// 4.7 TB/s.
 __global__ void kv_gather_kernel(const __grid_constant__ df_paged_kv c, const int32_t *start,
                                  const int32_t *n, int n_max, float *k_out, float *v_out,
                                  int32_t *status) {
