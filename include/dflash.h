@@ -645,7 +645,7 @@ typedef struct {
     const int32_t *seq_len;        /* device [batch]: valid rows of every sequence */
     int32_t n_pages, page_size;    /* page_size 16, 32, 64, 128 or 256 */
     int32_t max_pages;             /* page table entries per sequence */
-    int32_t batch;                 /* at most 4096 */
+    int32_t batch;                 /* at most 2048 */
     int32_t n_kv_heads, head_dim;  /* head_dim 64, 128 or 256 */
     float k_scale, v_scale;        /* powers of two (1 unless the values need another range) */
 } df_paged_kv;

@@ -54,10 +54,11 @@ int check_attention_paged(const df_paged_kv *c, int blk, int nq, bool shape_only
     REQ(blk > 0, DF_ESHAPE, "blk=%d", blk);
     REQ(nq > 0 && nq % c->n_kv_heads == 0, DF_ESHAPE, "nq=%d must be a positive multiple of n_kv_heads=%d",
         nq, c->n_kv_heads);
-    // units of work (32 keys of one KV head and 8 query rows) and row indices stay in 32 bits
+    // places of work (32 keys of one KV head and 8 query rows, and 24 more of each such task) and row
+    // indices stay in 32 bits
     const long long rows = (long long)blk * (nq / c->n_kv_heads);
     REQ(rows <= (1LL << 24), DF_ESHAPE, "blk x query heads per KV head = %lld", rows);
-    const double units = ((double)c->max_pages * c->page_size / 32 + 1) * c->batch * c->n_kv_heads *
+    const double units = ((double)c->max_pages * c->page_size / 32 + 25) * c->batch * c->n_kv_heads *
                          ((double)rows / 8 + 1);
     REQ(units < 1073741824.0, DF_ESHAPE, "%.3g pieces of 32 keys and 8 query rows (at most 2^30)", units);
     return DF_OK;

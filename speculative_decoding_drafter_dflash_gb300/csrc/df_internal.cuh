@@ -615,7 +615,7 @@ int launch_rollback(int32_t *seq_len, const int32_t *n, int B, int32_t *status, 
 constexpr int kOpsCounters = 4096;
 
 // Paged 4-bit KV cache (k_paged.cu, k_attn_paged.cu).
-constexpr int kPagedMaxBatch = 4096;
+constexpr int kPagedMaxBatch = 2048;    // (a CTA of the attention holds a word of each)
 constexpr int kPagedMaxAxes = 4;
 struct KvAppendArgs {
     df_paged_kv c;

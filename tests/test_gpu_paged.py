@@ -497,6 +497,18 @@ def test_attention_bad_tables_and_lengths_reach_the_status(shape):
         assert np.all(np.abs(got[1] - ref[1]) <= tol[1]), what
 
 
+@pytest.mark.parametrize("d,nq", [(64, 2), (128, 8), (256, 4), (256, 16)])
+def test_attention_of_the_largest_batch(d, nq):
+    # 2048 sequences of 0 to 5 cached rows and one new one, a page each
+    rng = np.random.default_rng(31)
+    lens = rng.integers(0, 6, 2048).tolist()
+    pool, host, q = _small(lens=lens, n_new=[1] * 2048, nq=nq, nkv=2, d=d, seed=17)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = _attend(pool, torch.tensor(q, device=DEV), _i32([1] * 2048), True, st).cpu().numpy()
+    ref, tol = _attend_ref(pool, host, q, [1] * 2048, True)
+    assert int(st) == 0 and np.all(np.abs(got - ref) <= tol)
+
+
 @pytest.mark.parametrize("nq", [4, 12])
 def test_attention_repeats_bit_for_bit_and_shares_a_workspace_between_sizes(nq):
     pool, host, q = _small(lens=(3000, 2999), n_new=(4, 4), nq=nq, seed=13, long=nq > 4)
@@ -545,6 +557,63 @@ def test_two_streams_and_a_captured_graph(nq):
     torch.cuda.synchronize()
     for o in outs:
         assert np.all(np.abs(o.cpu().numpy() - ref) <= tol)
+
+
+def test_two_graphs_share_a_workspace():
+    pool, host, q = _small(lens=(900, 850), n_new=(2, 2), seed=15)
+    other, ohost, oq = _small(lens=(70, 300), n_new=(9, 9), nq=4, d=256, seed=16, long=True)
+    ws = B.alloc_workspace(max(B.attention_paged_workspace_bytes(pool.cache, 2, 4),
+                               B.attention_paged_workspace_bytes(other.cache, 9, 4)))
+    work = []
+    for p, h, x, n in ((pool, host, q, [2, 2]), (other, ohost, oq, [9, 9])):
+        qt, nt = torch.tensor(x, device=DEV), _i32(n)
+        out = torch.zeros_like(qt)
+        _attend(p, qt, nt, True, ws=ws, out=out)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            _attend(p, qt, nt, True, ws=ws, out=out)
+        work.append((graph, out, qt, nt, *_attend_ref(p, h, x, n, True)))
+    for _ in range(3):
+        for graph, out, *_ in work:
+            out.zero_()
+            graph.replay()
+    torch.cuda.synchronize()
+    for _, out, _, _, ref, tol in work:
+        assert np.all(np.abs(out.cpu().numpy() - ref) <= tol)
+
+
+@pytest.mark.parametrize("blk", [1, 16])
+def test_pools_beyond_32_bits(blk):
+    nkv, d, page, nq, n = 8, 128, 256, 16, 600
+    pages = 2 ** 32 // (nkv * page * d // 2) + 40
+    if torch.cuda.mem_get_info()[0] < 16 << 30:
+        pytest.skip("needs 16 GB of device memory")
+    pools = [torch.empty((pages, nkv, page, d // w), dtype=torch.uint8, device=DEV) for w in (2, 16, 2, 16)]
+    width = 3 if blk == 1 else -(-10 ** 7 * 152 // (blk * nq // nkv * d * nkv * page))
+    table = torch.full((1, width), -1, dtype=torch.int32)
+    table[0, :3] = torch.tensor([pages - 1, 1, pages - 2])
+    seq = _i32([0])
+    cache = B.PagedKv(*pools, table.to(DEV), seq)
+    rng = np.random.default_rng(41)
+    k, v = (rng.standard_normal((1, n, nkv * d)).astype(np.float32) for _ in range(2))
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    B.kv_append_paged(cache, None, torch.tensor(k, device=DEV), torch.tensor(v, device=DEV), d_status=st)
+    seq.fill_(n)
+    ko, vo = (torch.zeros((1, nkv, n, d), device=DEV) for _ in range(2))
+    B.kv_gather_paged(cache, seq, ko, vo, d_status=st)
+    for got, x in ((ko, k), (vo, v)):
+        want = op.values(*op.quantise(x.reshape(n, nkv, d).astype(np.float64), 1.0), 1.0)
+        assert np.array_equal(got[0].cpu().numpy().transpose(1, 0, 2), want)
+    q = rng.standard_normal((1, blk, nq, d)).astype(np.float32)
+    out = torch.zeros((1, blk, nq, d), device=DEV)
+    ws = B.alloc_workspace(B.attention_paged_workspace_bytes(cache, blk, nq))
+    B.attention_paged(cache, torch.tensor(q, device=DEV), out, ws, d_status=st)
+    kk, vv = (x[0].cpu().numpy().astype(np.float64).transpose(1, 0, 2) for x in (ko, vo))
+    ref = op.attention(q[0], kk, vv, [n] * blk)
+    dx = 2.0 ** -19 * np.abs(q).max() * np.abs(kk).sum(-1).max() / np.sqrt(d)
+    assert int(st) == 0
+    assert np.abs(out[0].cpu().numpy() - ref).max() <= 2 * (dx + 2.0 ** -17) * np.abs(vv).max()
 
 
 def test_decode_loop():

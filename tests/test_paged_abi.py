@@ -31,7 +31,7 @@ BAD_CACHES = [
     (dict(page_size=8), "DF_ESHAPE", "page_size"), (dict(page_size=48), "DF_ESHAPE", "page_size"),
     (dict(page_size=512), "DF_ESHAPE", "page_size"), (dict(n_pages=0), "DF_ESHAPE", "n_pages"),
     (dict(max_pages=0), "DF_ESHAPE", "max_pages"), (dict(batch=0), "DF_ESHAPE", "batch"),
-    (dict(batch=4097), "DF_ESHAPE", "batch"), (dict(n_kv_heads=0), "DF_ESHAPE", "n_kv_heads"),
+    (dict(batch=2049), "DF_ESHAPE", "batch"), (dict(n_kv_heads=0), "DF_ESHAPE", "n_kv_heads"),
     (dict(max_pages=1 << 27), "DF_ESHAPE", "max_pages"),
     (dict(k_scale=0.75), "DF_EINVAL", "powers of two"), (dict(v_scale=0.0), "DF_EINVAL", "powers of two"),
     (dict(v_scale=float("nan")), "DF_EINVAL", "powers of two"),
@@ -113,7 +113,7 @@ def test_attention_refusals(L, kw, code, text):
 
 
 def test_attention_refuses_more_work_than_it_can_index(L):
-    c = _cache(L, max_pages=1 << 20, page_size=256, batch=4096, n_kv_heads=64)
+    c = _cache(L, max_pages=1 << 20, page_size=256, batch=2048, n_kv_heads=64)
     _refused(L, _attend(L, c, nq=64), "DF_ESHAPE", "pieces")
 
 
