@@ -58,6 +58,11 @@ __device__ __forceinline__ bool better(float av, int ai, float bv, int bi) {
     return av > bv || (av == bv && ai < bi);
 }
 
+struct alignas(8) Entry {
+    float v;
+    int i;
+};
+
 // A warp's running state: the best kp entries seen, sorted, one a lane (lanes >= kp are empty),
 // and over all others the lane's sums of e = 2^(c (x - mu)) and of e * log2(e).
 struct State {
@@ -174,13 +179,13 @@ __device__ __forceinline__ Raw<BF16> load(const uint8_t *base, int j, int mis, i
 
 // CTA (chunk, row). Bound: the logits, read once; per logit one conversion (16-bit), a running
 // maximum, half of three packed F32 operations, two single ones and the exponential.
-// 1024 rows of 248320 bf16 values with 20 alternatives: 141 us for 509 MB, 3.6 TB/s of the copy's 6.8, 117 us
+// 1024 rows of 248320 bf16 values with 20 alternatives: 140 us for 509 MB, 3.6 TB/s of the copy's 6.8, 117 us
 // with none; a row a CTA, four CTAs an SM, so 1024 rows are two rounds of 608, the second a third empty,
 // and 63% of the issue slots are taken. The list costs the difference: a step that may hold an entry
 // is looked through (30% of them), and the list is brought together five times a row. One row of
-// 248320 F32 values over 61 CTAs: 12.0 us, 16 rows of 262144: 18.3 us, latencies of a step, two sorts and a join.
-// (Two or three steps read ahead: 138 to 240 us; 7 CTAs of 4 warps an SM, all rows at once: 222 us;
-// entries ranked by all warps instead of sorted by one: 176 us, of spills.)
+// 248320 F32 values over 61 CTAs: 8.9 us, 16 rows of 262144: 15.6 us, the latencies of a step or two, a
+// sort, the arrival and the join. (Two or three steps read ahead: 138 to 240 us; 7 CTAs of 4 warps an
+// SM, all rows at once: 222 us; entries ranked by all warps instead of sorted by one: 176 us, of spills.)
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const __grid_constant__ LogprobsArgs a,
                                                                   int chunk, int n_chunks, float c) {
@@ -193,8 +198,9 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const __gri
     __shared__ float2 sums[kWarps];
     __shared__ float2 bound[kWarps];
     __shared__ int last;
-    __shared__ float held_v[kWarps][32 + kStep];   // entries on their way to the warp's list
+    __shared__ __align__(16) float held_v[kWarps][32 + kStep];   // entries on their way to the warp's list
     __shared__ int held_i[kWarps][32 + kStep];
+    __shared__ Entry slot[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int r = blockIdx.y + gridDim.y * blockIdx.z, ck = blockIdx.x;
     if (r >= a.R) return;
@@ -255,8 +261,8 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const __gri
                 m = fmaxf(m, held_v[w][at - from]);
             }
             follow(warp_max(m));
-            for (int base = 0; base < first[kWarps]; base += 32) {
-                const int at = base + lane;
+            for (int from0 = 0; from0 < first[kWarps]; from0 += 32) {
+                const int at = from0 + lane;
                 int w = 0, from = 0;
 #pragma unroll
                 for (int k = 1; k < kWarps; ++k) {
@@ -431,30 +437,6 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const __gri
         }
     }
 
-    // Joins the warps' states (all with one reference) in warp 0, in a fixed order.
-    auto join = [&](State &s) {
-        if (lane != 0) s.S = s.U = 0.f;
-        for (int half = kWarps / 2; half >= 1; half >>= 1) {
-            __syncthreads();
-            if (warp >= half && warp < 2 * half) {
-                slv[warp][lane] = s.lv;
-                sli[warp][lane] = s.li;
-                const float2 v = make_float2(warp_sum(s.S), warp_sum(s.U));
-                if (lane == 0) sums[warp] = v;
-            }
-            __syncthreads();
-            if (warp < half) {
-                s.merge(slv[warp + half][lane], sli[warp + half][lane], kp, c);
-                if (lane == 0) {
-                    s.S += sums[warp + half].x;
-                    s.U += sums[warp + half].y;
-                }
-            }
-        }
-        s.S = warp_sum(s.S);
-        s.U = warp_sum(s.U);
-    };
-
     // The token's own logit, on its way while the lists are joined.
     int tk = -1;
     float tx = 0.f;
@@ -482,43 +464,73 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const __gri
         __syncthreads();
         if (!last) return;
         fetch();
-        M = -INFINITY;
-        for (int k = lane; k < n_chunks; k += 32) M = fmaxf(M, __ldcg(&parts[k].v[0]));
-        M = warp_max(M);
-        st.lv = -INFINITY;
-        st.li = kNone;
-        st.mu = M;
-        st.S = st.U = 0.f;
-        for (int k0 = warp; k0 < n_chunks; k0 += 4 * kWarps) {
-            float v[4], om[4], oS[4], oU[4];
-            int i[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int k = min(k0 + u * kWarps, n_chunks - 1);
-                om[u] = __ldcg(&parts[k].v[0]);
-                oS[u] = __ldcg(&parts[k].S);
-                oU[u] = __ldcg(&parts[k].U);
-                v[u] = __ldcg(&parts[k].v[lane]);
-                i[u] = __ldcg(&parts[k].i[lane]);
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                if (k0 + u * kWarps >= n_chunks) break;
-                State o;
-                o.mu = om[u];
-                o.S = oS[u];
-                o.U = oU[u];
-                o.rebase(M, c);
-                if (lane == 0) {
-                    st.S += o.S;
-                    st.U += o.U;
-                }
-                st.merge(v[u], i[u], kp, c);
-            }
+        // A thread is a chunk: its maximum's place among all, and its sums against the largest. An
+        // entry that is l-th of its chunk, whose maximum is r-th, has r + l better ones at least, so
+        // only kp (kp + 1) / 2 of them can be among the best; they are put by (r, l) and counted
+        // out. (A warp's merges of the lists in turn took 4 us for 61 chunks.)
+        float *const top_v = &held_v[0][0];                        // [n_chunks]
+        int *const place = &held_i[0][0];                          // [n_chunks]
+        Entry *const cand = reinterpret_cast<Entry *>(top_v + kThreads);   // [n_cand]
+        const int n_cand = kp * (kp + 1) / 2;
+        const int tid = threadIdx.x;
+        float tv = -INFINITY, pS = 0.f, pU = 0.f;
+        if (tid < n_chunks) {
+            tv = __ldcg(&parts[tid].v[0]);
+            pS = __ldcg(&parts[tid].S);
+            pU = __ldcg(&parts[tid].U);
         }
-        st.S = warp_sum(st.S);
-        st.U = warp_sum(st.U);
-        join(st);
+        const int e0 = tid, k0 = min(e0 / kp, n_chunks - 1);       // the first entry is on its way too
+        const float v0 = __ldcg(&parts[k0].v[e0 % kp]);
+        const int i0 = __ldcg(&parts[k0].i[e0 % kp]);
+        top_v[tid] = tv;
+        for (int k = tid; k < n_cand; k += kThreads) cand[k] = Entry{-INFINITY, kNone};
+        const float wm = warp_max(tv);
+        if (lane == 0) bound[warp].x = wm;
+        __syncthreads();
+        M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, bound[w].x);
+        int rank = 0;
+        if (tid < n_chunks) {
+#pragma unroll 8
+            for (int k = 0; k < n_chunks; ++k) rank += better(top_v[k], k, tv, tid);
+            place[tid] = rank;
+        }
+        st.mu = tv;
+        st.S = pS;
+        st.U = pU;
+        st.rebase(M, c);
+        st.mu = M;                           // (a chunk of -inf and threads without one hold no sums)
+        __syncthreads();
+        for (int e = tid; e < n_chunks * kp; e += kThreads) {
+            const int k = e / kp, l = e - k * kp, at = place[k];
+            const float v = e == e0 ? v0 : __ldcg(&parts[k].v[l]);
+            const int i = e == e0 ? i0 : __ldcg(&parts[k].i[l]);
+            if (at + l < kp) cand[at * kp - at * (at - 1) / 2 + l] = Entry{v, i};
+            else st.drop(v, i, c);
+        }
+        if (tid < 32) slot[tid] = Entry{-INFINITY, kNone};
+        __syncthreads();
+        for (int e = tid; e < n_cand; e += kThreads) {
+            const Entry x = cand[e];
+            if (x.i == kNone) continue;
+            int at = 0;
+#pragma unroll 8
+            for (int k = 0; k < n_cand; ++k) at += better(cand[k].v, cand[k].i, x.v, x.i);
+            if (at < kp) slot[at] = x;
+            else st.drop(x.v, x.i, c);
+        }
+        const float wS = warp_sum(st.S), wU = warp_sum(st.U);
+        if (lane == 0) sums[warp] = make_float2(wS, wU);
+        __syncthreads();
+        st.lv = slot[lane].v;
+        st.li = slot[lane].i;
+        st.S = st.U = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            st.S += sums[w].x;
+            st.U += sums[w].y;
+        }
     } else {
         fetch();
     }
@@ -560,6 +572,8 @@ Plan plan_of(int R, int V) {
     const long long target = 4LL * sm_count();
     long long chunk = ((long long)R * V + target - 1) / target;
     chunk = (chunk + step - 1) / step * step;
+    const long long most = ((V + 7LL) / kThreads + step) / step * step;       // a thread joins a chunk
+    if (chunk < most) chunk = most;
     if (R > kOpsCounters || chunk > V + 7LL) chunk = (V + 7LL + step - 1) / step * step;
     Plan p;
     p.chunk = (int)chunk;

@@ -87,6 +87,18 @@ def test_ties_go_to_the_lowest_index():
     _check(-x[[0, 1, 3]], [0, 5, 0], 32)
 
 
+def test_the_largest_rows_and_lists_over_many_chunks():
+    g = torch.Generator(device=DEV).manual_seed(8)
+    x = torch.randn((1, 2600001), generator=g, device=DEV)
+    _check(x, [2600000], 32)
+    _check(x.to(torch.bfloat16)[:, 1:], [3], 32)          # (few distinct values at the top)
+    x = torch.randint(0, 3, (2, 400001), generator=g, device=DEV).float()
+    x[1, :399990] -= 5.0                                  # the best all in the last chunk, fewer than the list
+    _check(x, [0, 400000], 32)
+    x[0, 4096:] = -math.inf                               # whole chunks without a probability
+    _check(x, [1, 2], 31)
+
+
 def test_masked_rows_and_few_left():
     V = 20000
     g = torch.Generator(device=DEV).manual_seed(5)
