@@ -288,69 +288,73 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1) attn_paged_tc_kernel(
                 return x < p.x1 && key < p.keys ? table[key >> pshift] : -1;
             };
             int page = pages(p.x0);
-            const int qb = seg % C::kQBufs;
-            if (seg >= C::kQBufs) wait(&q_free[qb], seg / C::kQBufs - 1);
-            uint8_t *qs = qbuf + qb * C::kQBytes;
-            // A warp's rows, QR loaded at a time; lane k looks after row k of them.
-            constexpr int WR = NP / kLoadWarps, QR = WR < 4 ? WR : 4;
-            const int mine = lw * WR + (lane < WR ? lane : 0);
-            const size_t my_off = mine < p.nr ? row_offset(a, p, mine) : 0;
-            float my_up = 1.f;
-            // log2(e) / sqrt(d) is taken into q, so that a row's scale is a power of two
-            const float unit = kLog2e / sqrtf((float)D);
-            auto scaled = [&](float4 f) { return make_float4(f.x * unit, f.y * unit, f.z * unit, f.w * unit); };
-            for (int k0 = 0; k0 < WR; k0 += QR) {
-                float4 v[QR][D / 128];
+            // The query rows come after the tiles that the ring has places for: those need nothing of
+            // them, and the rows' place is free only when the piece before is done.
+            auto query_rows = [&]() {
+                const int qb = seg % C::kQBufs;
+                if (seg >= C::kQBufs) wait(&q_free[qb], seg / C::kQBufs - 1);
+                uint8_t *qs = qbuf + qb * C::kQBytes;
+                // A warp's rows, QR loaded at a time; lane k looks after row k of them.
+                constexpr int WR = NP / kLoadWarps, QR = WR < 4 ? WR : 4;
+                const int mine = lw * WR + (lane < WR ? lane : 0);
+                const size_t my_off = mine < p.nr ? row_offset(a, p, mine) : 0;
+                float my_up = 1.f;
+                // log2(e) / sqrt(d) is taken into q, so that a row's scale is a power of two
+                const float unit = kLog2e / sqrtf((float)D);
+                auto scaled = [&](float4 f) { return make_float4(f.x * unit, f.y * unit, f.z * unit, f.w * unit); };
+                for (int k0 = 0; k0 < WR; k0 += QR) {
+                    float4 v[QR][D / 128];
 #pragma unroll
-                for (int k = 0; k < QR; ++k) {
-                    const float *src = a.q + __shfl_sync(0xffffffffu, my_off, k0 + k) + 4 * lane;
+                    for (int k = 0; k < QR; ++k) {
+                        const float *src = a.q + __shfl_sync(0xffffffffu, my_off, k0 + k) + 4 * lane;
 #pragma unroll
-                    for (int hf = 0; hf < D / 128; ++hf) {
-                        v[k][hf] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (lw * WR + k0 + k < p.nr) v[k][hf] = scaled(*reinterpret_cast<const float4 *>(src + 128 * hf));
+                        for (int hf = 0; hf < D / 128; ++hf) {
+                            v[k][hf] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (lw * WR + k0 + k < p.nr) v[k][hf] = scaled(*reinterpret_cast<const float4 *>(src + 128 * hf));
+                        }
+                    }
+                    float amax[QR];
+#pragma unroll
+                    for (int k = 0; k < QR; ++k) {
+                        amax[k] = 0.f;
+#pragma unroll
+                        for (int hf = 0; hf < D / 128; ++hf)
+                            amax[k] = fmaxf(fmaxf(amax[k], fmaxf(fabsf(v[k][hf].x), fabsf(v[k][hf].y))),
+                                            fmaxf(fabsf(v[k][hf].z), fabsf(v[k][hf].w)));
+                    }
+#pragma unroll
+                    for (int m = 16; m >= 1; m >>= 1)
+#pragma unroll
+                        for (int k = 0; k < QR; ++k) amax[k] = fmaxf(amax[k], __shfl_xor_sync(0xffffffffu, amax[k], m));
+#pragma unroll
+                    for (int k = 0; k < QR; ++k) {
+                        const int rr = lw * WR + k0 + k;
+                        float down, up;
+                        row_scale(amax[k], down, up);
+                        if (lane == k0 + k) my_up = up;
+#pragma unroll
+                        for (int hf = 0; hf < D / 128; ++hf) {
+                            uint2 h, lo;
+                            split_f16(v[k][hf].x * down, v[k][hf].y * down, h.x, lo.x);
+                            split_f16(v[k][hf].z * down, v[k][hf].w * down, h.y, lo.y);
+                            // dims 128 hf + 4 lane .. + 3 of rows rr (hi) and NP + rr (lo)
+                            uint8_t *o = qs + (2 * hf + (lane >> 4)) * (2 * NP * 128) + rr * 128 +
+                                         (((((lane & 15) >> 1)) ^ (rr & 7)) << 4) + (lane & 1) * 8;
+                            *reinterpret_cast<uint2 *>(o) = h;
+                            *reinterpret_cast<uint2 *>(o + NP * 128) = lo;   // (NP is a multiple of 8)
+                        }
                     }
                 }
-                float amax[QR];
-#pragma unroll
-                for (int k = 0; k < QR; ++k) {
-                    amax[k] = 0.f;
-#pragma unroll
-                    for (int hf = 0; hf < D / 128; ++hf)
-                        amax[k] = fmaxf(fmaxf(amax[k], fmaxf(fabsf(v[k][hf].x), fabsf(v[k][hf].y))),
-                                        fmaxf(fabsf(v[k][hf].z), fabsf(v[k][hf].w)));
+                if (lane < WR) {
+                    rscale[qb * NP + mine] = a.c.k_scale * my_up;
+                    rlim[qb * NP + mine] = mine < p.nr ? row_limit(a, p, mine) : 0;
+                    roff[qb * NP + mine] = my_off;
                 }
-#pragma unroll
-                for (int m = 16; m >= 1; m >>= 1)
-#pragma unroll
-                    for (int k = 0; k < QR; ++k) amax[k] = fmaxf(amax[k], __shfl_xor_sync(0xffffffffu, amax[k], m));
-#pragma unroll
-                for (int k = 0; k < QR; ++k) {
-                    const int rr = lw * WR + k0 + k;
-                    float down, up;
-                    row_scale(amax[k], down, up);
-                    if (lane == k0 + k) my_up = up;
-#pragma unroll
-                    for (int hf = 0; hf < D / 128; ++hf) {
-                        uint2 h, lo;
-                        split_f16(v[k][hf].x * down, v[k][hf].y * down, h.x, lo.x);
-                        split_f16(v[k][hf].z * down, v[k][hf].w * down, h.y, lo.y);
-                        // dims 128 hf + 4 lane .. + 3 of rows rr (hi) and NP + rr (lo)
-                        uint8_t *o = qs + (2 * hf + (lane >> 4)) * (2 * NP * 128) + rr * 128 +
-                                     (((((lane & 15) >> 1)) ^ (rr & 7)) << 4) + (lane & 1) * 8;
-                        *reinterpret_cast<uint2 *>(o) = h;
-                        *reinterpret_cast<uint2 *>(o + NP * 128) = lo;   // (NP is a multiple of 8)
-                    }
-                }
-            }
-            if (lane < WR) {
-                rscale[qb * NP + mine] = a.c.k_scale * my_up;
-                rlim[qb * NP + mine] = mine < p.nr ? row_limit(a, p, mine) : 0;
-                roff[qb * NP + mine] = my_off;
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&q_full[qb]);
-            for (int x = p.x0; x < p.x1; ++x, ++n) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&q_full[qb]);
+            };
+            auto tile = [&](int x) {
                 const int st = n % C::kRawStages;
                 const int now = page;
                 page = pages(x + 1);
@@ -385,7 +389,13 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1) attn_paged_tc_kernel(
                     }
                 }
                 cp_arrive(&raw_full[st]);
-            }
+            };
+            const int rows_at = p.x0 + min(C::kRawStages, p.x1 - p.x0);
+#pragma unroll 1
+            for (int x = p.x0; x < rows_at; ++x, ++n) tile(x);
+            query_rows();
+#pragma unroll 1
+            for (int x = rows_at; x < p.x1; ++x, ++n) tile(x);
             ++seg;
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
