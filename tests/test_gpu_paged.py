@@ -497,15 +497,16 @@ def test_attention_bad_tables_and_lengths_reach_the_status(shape):
         assert np.all(np.abs(got[1] - ref[1]) <= tol[1]), what
 
 
-@pytest.mark.parametrize("d,nq", [(64, 2), (128, 8), (256, 4), (256, 16)])
-def test_attention_of_the_largest_batch(d, nq):
-    # 2048 sequences of 0 to 5 cached rows and one new one, a page each
+@pytest.mark.parametrize("d,nq,batch,long", [(64, 2, 2048, False), (128, 8, 2048, False), (256, 4, 2048, False),
+                                             (256, 16, 2048, False), (128, 24, 1500, True), (256, 24, 1100, True)])
+def test_attention_of_the_largest_batch(d, nq, batch, long):
+    # sequences of 0 to 5 cached rows and one new one, a page each
     rng = np.random.default_rng(31)
-    lens = rng.integers(0, 6, 2048).tolist()
-    pool, host, q = _small(lens=lens, n_new=[1] * 2048, nq=nq, nkv=2, d=d, seed=17)
+    lens = rng.integers(0, 6, batch).tolist()
+    pool, host, q = _small(lens=lens, n_new=[1] * batch, nq=nq, nkv=2, d=d, seed=17, long=long)
     st = torch.zeros(1, dtype=torch.int32, device=DEV)
-    got = _attend(pool, torch.tensor(q, device=DEV), _i32([1] * 2048), True, st).cpu().numpy()
-    ref, tol = _attend_ref(pool, host, q, [1] * 2048, True)
+    got = _attend(pool, torch.tensor(q, device=DEV), _i32([1] * batch), True, st).cpu().numpy()
+    ref, tol = _attend_ref(pool, host, q, [1] * batch, True)
     assert int(st) == 0 and np.all(np.abs(got - ref) <= tol)
 
 
