@@ -12,14 +12,15 @@
 //
 // A warp takes 32 keys a step, 8 warps a piece of a task in turn, each with a ring of its own, a
 // reference, sums and outputs; they meet at the piece's end. No warp waits for another in between.
-// Bound: for few rows the instructions that turn codes into operands (64 conversions, 64 products
-// and 48 matrix instructions a thread and step; 60% of the issue slots are taken by 16 warps an SM),
-// not the cache's bytes: 64 single tokens over up to 8191 keys each (16/8 heads of 128) 81 us, 312 MB at
-// 3.9 TB/s, with one matrix instruction for hi and lo, 91 us with two. From 5 rows on the matrix rate
-// (mma.sync gives half of it here to tcgen05): 8 x 32768 keys, 16/8 heads: 16 rows a head 122 us, 32 rows 233 us. One
-// token over 8192 keys (24/4 heads of 256) 14.2 us, a block of 16 over 4096 (16/8 of 128) 14.0 us: a
-// chain of latencies (lengths and line 1.9 us, pages, rows and first keys 2.2, a step or two 3.5, the
-// warps' join 1.5, the parts' 3.5).
+// Bound: for few rows the instructions that turn codes into operands (144 conversions, 128 products
+// and 32 to 96 matrix instructions of the 740 of a warp and step; 60% of the issue slots are taken
+// by 16 warps an SM), not the cache's bytes: 64 single tokens over up to 8191 keys each (16/8 heads of
+// 128) 74 us, 312 MB at 4.2 TB/s (hi and lo in one matrix instruction took 10 us off, copies without
+// branches, with zeros where there is no row, 7). From 5 rows on the matrix rate (mma.sync gives half of it
+// here to tcgen05): 8 x 32768 keys, 16/8 heads: 16 rows a head 110 us, 32 rows 208 us. One token over 8192
+// keys (24/4 heads of 256) 14.2 us, a block of 16 over 4096 (16/8 of 128) 13.6 us: a chain of latencies
+// (lengths and line 1.9 us, pages, rows and first keys 2.2, a step or two 3.5, the warps' join 1.5, the
+// parts' 3.5).
 #include "attn_paged.cuh"
 
 namespace df {
@@ -49,6 +50,21 @@ __device__ __forceinline__ void cp_wait() {
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<unsigned long long &>(r))
+        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<unsigned long long &>(r))
+        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)),
+          "l"(reinterpret_cast<unsigned long long &>(c)));
     return r;
 }
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -146,9 +162,12 @@ __global__ void __launch_bounds__(32 * kWarps, D * NT <= 128 ? 2 : 1)
             const int c = lane + 32 * k, r = c / L::kChunks;
             place[k] = r * (D / 2) + (((c % L::kChunks) ^ L::swz(r)) << 4);
         }
-        const int sc_at = (lane % SC) * 16;
-        const uint8_t *sc_from = (lane < SC ? a.c.k_scales : a.c.v_scales) + sc_at;
-        const uint32_t sc_place = 2 * L::kCodes + (lane < SC ? 0 : L::kScales) + sc_at;
+        // Up to 128 dims one copy takes the scales of both groups (group lane / (2 SC)).
+        constexpr bool kBoth = 4 * SC <= 32;
+        const int sc_at = (lane % SC) * 16, sc_group = kBoth ? (lane / (2 * SC)) & 1 : 0;
+        const bool sc_k = (lane % (2 * SC)) < SC;
+        const uint8_t *sc_from = (sc_k ? a.c.k_scales : a.c.v_scales) + sc_at;
+        const uint32_t sc_place = 2 * L::kCodes + (sc_k ? 0 : L::kScales) + sc_at + sc_group * D;
         // Pages of a step's two groups.
         auto pages_of = [&](int x, int (&pg)[2]) {
 #pragma unroll
@@ -160,27 +179,30 @@ __global__ void __launch_bounds__(32 * kWarps, D * NT <= 128 ? 2 : 1)
         auto issue = [&](int x, int stage, const int (&pg)[2]) {
             if (x >= x1) return;
             const uint32_t st = my_at + stage * L::kStage;
+            // Scales of rows past the last are zeros, so those rows are zeros whatever the page
+            // holds; a group without a row (or without a page) is not read at all.
+            size_t row[2];
+            int left[2];
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                const int key = x * kUnit + 16 * s, left = p.keys - key;   // valid rows from here on
-                const bool good = (unsigned)pg[s] < (unsigned)a.c.n_pages, ok = good && left > 0;
-                if (!good) set_status(a.status, DF_EINVAL);
-                const size_t row = ok ? (size_t)(unsigned)pg[s] * page_rows + (head_rows + (key & mask)) : 0;
-                if (ok) {
-                    const uint8_t *kc = a.c.k_codes + row * (D / 2) + lane * 16, *vc = a.c.v_codes + row * (D / 2) + lane * 16;
+                const int key = x * kUnit + 16 * s;
+                const bool good = (unsigned)pg[s] < (unsigned)a.c.n_pages;
+                left[s] = good ? p.keys - key : 0;                 // valid rows from here on
+                row[s] = (size_t)(unsigned)(good ? pg[s] : 0) * page_rows + (head_rows + (key & mask));
+                const size_t from = row[s] * (D / 2) + lane * 16;
+                const int bytes = left[s] > 0 ? 16 : 0;
 #pragma unroll
-                    for (int k = 0; k < PL; ++k) {
-                        cp16(st + 16 * s * (D / 2) + place[k], kc + 512 * k, 16);
-                        cp16(st + L::kCodes + 16 * s * (D / 2) + place[k], vc + 512 * k, 16);
-                    }
+                for (int k = 0; k < PL; ++k) {
+                    cp16(st + 16 * s * (D / 2) + place[k], a.c.k_codes + from + 512 * k, bytes);
+                    cp16(st + L::kCodes + 16 * s * (D / 2) + place[k], a.c.v_codes + from + 512 * k, bytes);
                 }
-                // Scales of rows past the last are zeros, so those rows are zeros whatever the
-                // page holds.
-                if (lane < 2 * SC) {
-                    const int bytes = ok ? min(max(left * SC - sc_at, 0), 16) : 0;
-                    cp16(st + sc_place + s * D, bytes ? sc_from + row * SC : a.c.k_scales, bytes);
-                }
+                if constexpr (!kBoth) cp16(st + sc_place + s * D, sc_from + row[s] * SC, min(max(left[s] * SC - sc_at, 0), 16));
             }
+            if constexpr (kBoth)
+                if (lane < 4 * SC)
+                    cp16(st + sc_place, sc_from + (sc_group ? row[1] : row[0]) * SC,
+                         min(max((sc_group ? left[1] : left[0]) * SC - sc_at, 0), 16));
+            if ((unsigned)pg[0] >= (unsigned)a.c.n_pages || (unsigned)pg[1] >= (unsigned)a.c.n_pages) set_status(a.status, DF_EINVAL);
         };
 
         int pg[2];
@@ -358,7 +380,12 @@ __global__ void __launch_bounds__(32 * kWarps, D * NT <= 128 ? 2 : 1)
 #pragma unroll
                 for (int sb = 0; sb < 2; ++sb)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[sb][0][e] += __shfl_xor_sync(0xffffffffu, s[sb][0][e], 2);
+                    for (int e = 0; e < 4; e += 2) {
+                        const float2 v = add2(make_float2(s[sb][0][e], s[sb][0][e + 1]),
+                                              make_float2(__shfl_xor_sync(0xffffffffu, s[sb][0][e], 2),
+                                                          __shfl_xor_sync(0xffffffffu, s[sb][0][e + 1], 2)));
+                        s[sb][0][e] = v.x, s[sb][0][e + 1] = v.y;
+                    }
             }
             // The keys a row may not see drop out.
             const int key0 = x * kUnit;
@@ -385,7 +412,11 @@ __global__ void __launch_bounds__(32 * kWarps, D * NT <= 128 ? 2 : 1)
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) ex[sb][n][e] = fmaf(s[sb][n][e], rs[n][e & 1], -m[n][e & 1]);
+                        for (int e = 0; e < 4; e += 2) {
+                            const float2 v = fma2(make_float2(s[sb][n][e], s[sb][n][e + 1]), make_float2(rs[n][0], rs[n][1]),
+                                                  make_float2(-m[n][0], -m[n][1]));
+                            ex[sb][n][e] = v.x, ex[sb][n][e + 1] = v.y;
+                        }
                         top = fmaxf(top, fmaxf(fmaxf(ex[sb][n][0], ex[sb][n][1]), fmaxf(ex[sb][n][2], ex[sb][n][3])));
                     }
             };
@@ -424,8 +455,8 @@ __global__ void __launch_bounds__(32 * kWarps, D * NT <= 128 ? 2 : 1)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const float p0 = ex2(ex[sb][n][2 * e]), p1 = ex2(ex[sb][n][2 * e + 1]);
-                        l[n][0] += p0;
-                        l[n][1] += p1;
+                        const float2 sum = add2(make_float2(l[n][0], l[n][1]), make_float2(p0, p1));
+                        l[n][0] = sum.x, l[n][1] = sum.y;
                         uint32_t hh, ll;
                         split_f16(p0, p1, hh, ll);
                         if constexpr (PAIRS) {

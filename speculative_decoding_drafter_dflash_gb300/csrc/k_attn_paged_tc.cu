@@ -21,7 +21,7 @@
 //
 // 8 sequences of 32768 keys, 32 rows a head (16/8 heads of 128): 139 us, 304 MB at 2.2 TB/s and 247 TFLOP/s
 // (twice that with the lo halves; the tensor pipe is busy 21% of the time); the mma.sync kernel takes
-// 233 us.
+// 208 us.
 // What bounds it is neither: a tile is 1.3 us, of which 2/3 of the issue slots are taken, and the
 // rest is the chain from a tile's codes to its outputs, three roles long, at two tiles in flight.
 #include "attn_paged.cuh"
@@ -56,17 +56,16 @@ struct Cfg {
     static constexpr int kScales = kTile * D / 16;
     static constexpr int kRaw = 2 * kCodes + 2 * kScales;
     // As deep as shared memory allows: a tile's bytes are 2 to 3 us on their way.
-    static constexpr int kRawStages = D == 128 ? (NP == 32 ? 4 : 5) : 2;
+    static constexpr int kRawStages = D == 128 ? 4 : 2;
     static constexpr int kVBytes = kTile * 128 * 2;           // 128 dims of a tile's V, FP16
     static constexpr int kVBufs = 2;
     static constexpr int kPBytes = kTile * 128;               // a tile's P: 128-byte rows
     static constexpr int kQBytes = 2 * NP * D * 2;
-    static constexpr int kQBufs = D == 128 && NP < 32 ? 2 : 1;
     static constexpr int kAccBytes = 2 * NP * D * 4;          // F32 outputs: [group][row][D]
-    static constexpr int kBars = 2 * kRawStages + 2 + 2 * kVBufs + 2 + 2 + 2 + 2 + 2 * kQBufs + 2;
-    static constexpr size_t kFixed = 1024 + (size_t)kVBufs * kVBytes + 2 * kPBytes + kQBufs * kQBytes +
+    static constexpr int kBars = 2 * kRawStages + 2 + 2 * kVBufs + 2 + 2 + 2 + 2 + 2 + 2;
+    static constexpr size_t kFixed = 1024 + (size_t)kVBufs * kVBytes + 2 * kPBytes + kQBytes +
                                      kRawStages * kRaw + kAccBytes + kBars * 8 + 64 * 4 +
-                                     (size_t)NP * 4 * (4 * kQBufs + 8 + 2 + 2) + 64;
+                                     (size_t)NP * 4 * (4 + 8 + 2 + 2) + 64;
     // TMEM columns: two K operands, two score tiles, the groups' outputs
     static constexpr int kKCols = D / 2;
     static constexpr int kS = 2 * kKCols, kO = kS + 4 * NP, kOCols = kHalves * 2 * NP;
@@ -198,7 +197,7 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1) attn_paged_tc_kernel(
     uint8_t *vbuf = smem;
     uint8_t *pbuf = vbuf + C::kVBufs * C::kVBytes;
     uint8_t *qbuf = pbuf + 2 * C::kPBytes;
-    uint8_t *raw = qbuf + C::kQBufs * C::kQBytes;
+    uint8_t *raw = qbuf + C::kQBytes;
     float *accs = reinterpret_cast<float *>(raw + C::kRawStages * C::kRaw);
     uint64_t *bar = reinterpret_cast<uint64_t *>(reinterpret_cast<uint8_t *>(accs) + C::kAccBytes);
     uint64_t *raw_full = bar, *raw_free = raw_full + C::kRawStages;
@@ -207,13 +206,13 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1) attn_paged_tc_kernel(
     uint64_t *qk_done = v_free + C::kVBufs;                    // [2] scores ready, K operand free
     uint64_t *s_free = qk_done + 2, *p_full = s_free + 2;      // [2] each
     uint64_t *pv_done = p_full + 2;                            // [2] outputs added, P free
-    uint64_t *q_full = pv_done + 2, *q_free = q_full + C::kQBufs;
-    uint64_t *drain = q_free + C::kQBufs;                      // [2]
+    uint64_t *q_full = pv_done + 2, *q_free = q_full + 1;
+    uint64_t *drain = q_free + 1;                              // [2]
     int *misc = reinterpret_cast<int *>(drain + 2);            // [64]
-    float *rscale = reinterpret_cast<float *>(misc + 64);      // [kQBufs][NP]
-    int *rlim = reinterpret_cast<int *>(rscale + C::kQBufs * NP);
-    size_t *roff = reinterpret_cast<size_t *>(rlim + C::kQBufs * NP);   // row_offset of every row
-    float *red = reinterpret_cast<float *>(roff + C::kQBufs * NP);      // [2 groups][4][NP]
+    float *rscale = reinterpret_cast<float *>(misc + 64);      // [NP]
+    int *rlim = reinterpret_cast<int *>(rscale + NP);
+    size_t *roff = reinterpret_cast<size_t *>(rlim + NP);   // row_offset of every row
+    float *red = reinterpret_cast<float *>(roff + NP);      // [2 groups][4][NP]
     float *ref = red + 8 * NP, *rl = ref + 2 * NP;             // [2][NP] negatives of the references; [2][NP] sums
     uint32_t *tslot = reinterpret_cast<uint32_t *>(rl + 2 * NP);
     int *abort_flag = reinterpret_cast<int *>(tslot + 1);
@@ -239,10 +238,8 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1) attn_paged_tc_kernel(
             mbar_init(&v_full[i], 4);
             mbar_init(&v_free[i], 1);
         }
-        for (int i = 0; i < C::kQBufs; ++i) {
-            mbar_init(&q_full[i], kLoadWarps);
-            mbar_init(&q_free[i], kSoftWarps);
-        }
+        mbar_init(q_full, kLoadWarps);
+        mbar_init(q_free, kSoftWarps);
         mbar_init(&drain[0], 1);
         mbar_init(&drain[1], 1);
         *abort_flag = 0;
@@ -291,9 +288,7 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1) attn_paged_tc_kernel(
             // The query rows come after the tiles that the ring has places for: those need nothing of
             // them, and the rows' place is free only when the piece before is done.
             auto query_rows = [&]() {
-                const int qb = seg % C::kQBufs;
-                if (seg >= C::kQBufs) wait(&q_free[qb], seg / C::kQBufs - 1);
-                uint8_t *qs = qbuf + qb * C::kQBytes;
+                if (seg > 0) wait(q_free, seg - 1);
                 // A warp's rows, QR loaded at a time; lane k looks after row k of them.
                 constexpr int WR = NP / kLoadWarps, QR = WR < 4 ? WR : 4;
                 const int mine = lw * WR + (lane < WR ? lane : 0);
@@ -338,7 +333,7 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1) attn_paged_tc_kernel(
                             split_f16(v[k][hf].x * down, v[k][hf].y * down, h.x, lo.x);
                             split_f16(v[k][hf].z * down, v[k][hf].w * down, h.y, lo.y);
                             // dims 128 hf + 4 lane .. + 3 of rows rr (hi) and NP + rr (lo)
-                            uint8_t *o = qs + (2 * hf + (lane >> 4)) * (2 * NP * 128) + rr * 128 +
+                            uint8_t *o = qbuf + (2 * hf + (lane >> 4)) * (2 * NP * 128) + rr * 128 +
                                          (((((lane & 15) >> 1)) ^ (rr & 7)) << 4) + (lane & 1) * 8;
                             *reinterpret_cast<uint2 *>(o) = h;
                             *reinterpret_cast<uint2 *>(o + NP * 128) = lo;   // (NP is a multiple of 8)
@@ -346,13 +341,13 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1) attn_paged_tc_kernel(
                     }
                 }
                 if (lane < WR) {
-                    rscale[qb * NP + mine] = a.c.k_scale * my_up;
-                    rlim[qb * NP + mine] = mine < p.nr ? row_limit(a, p, mine) : 0;
-                    roff[qb * NP + mine] = my_off;
+                    rscale[mine] = a.c.k_scale * my_up;
+                    rlim[mine] = mine < p.nr ? row_limit(a, p, mine) : 0;
+                    roff[mine] = my_off;
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&q_full[qb]);
+                if (lane == 0) mbar_arrive(q_full);
             };
             auto tile = [&](int x) {
                 const int st = n % C::kRawStages;
@@ -414,9 +409,8 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1) attn_paged_tc_kernel(
         while (u < u_end && ok) {
             const Piece p = next_piece<kTile, NP, kExtra>(a, line, off, u, u_end);
             if (!outputs) {
-                const int qb = seg % C::kQBufs;
-                const uint64_t bq = sw128_desc(smem_u32(qbuf + qb * C::kQBytes));
-                ok = ok && wait(&q_full[qb], seg / C::kQBufs);
+                const uint64_t bq = sw128_desc(smem_u32(qbuf));
+                ok = ok && wait(q_full, seg);
                 for (int x = p.x0; x < p.x1 && ok; ++x, ++n) {
                     if (n >= 2) ok = wait(&s_free[n & 1], (n >> 1) - 1);
                     ok = ok && wait(&k_full[n & 1], n >> 1);
@@ -576,7 +570,6 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1) attn_paged_tc_kernel(
         int n = 0, seg = 0;
         while (u < u_end) {
             const Piece p = next_piece<kTile, NP, kExtra>(a, line, off, u, u_end);
-            const int qb = seg % C::kQBufs;
             // Sums of pairs of rows; the references' negatives are one for the group and lie in
             // shared memory: at first a value below any score, finite so that a masked score
             // stays -inf against it.
@@ -589,11 +582,11 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1) attn_paged_tc_kernel(
 #pragma unroll
                 for (int i = 0; i < HR; ++i) acc(hf, i) = 0.f;
             if (gt < NP) gref[gt] = -kLowest;
-            wait(&q_full[qb], seg / C::kQBufs);
-            const float2 *rs2 = reinterpret_cast<const float2 *>(rscale + qb * NP + r0);
-            const int *lim = rlim + qb * NP + r0;
+            wait(q_full, seg);
+            const float2 *rs2 = reinterpret_cast<const float2 *>(rscale + r0);
+            const int *lim = rlim + r0;
             int lim_min = 0x7fffffff;
-            for (int r = 0; r < p.nr; ++r) lim_min = min(lim_min, rlim[qb * NP + r]);
+            for (int r = 0; r < p.nr; ++r) lim_min = min(lim_min, rlim[r]);
             int pending = 0, mine = 0;                         // tiles in the TMEM outputs; tiles so far
             // Tiles up to i join the F32 sums.
             auto flush = [&](int i) {
@@ -742,7 +735,6 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1) attn_paged_tc_kernel(
             all_sync();
             // The groups' results joined: every thread takes its dims of every other row.
             float *part = part_of<D, NP>(a, p.first, (int)blockIdx.x);
-            const size_t *row_of = roff + qb * NP;
             auto factors = [&](int r, float &f0, float &f1) {
                 const float m0 = -ref[r], m1 = -ref[NP + r], m = fmaxf(m0, m1);
                 f0 = ex2(m0 - m);
@@ -752,7 +744,7 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1) attn_paged_tc_kernel(
             for (int r = grp * C::kSplit + (r0 ? 1 : 0); r < p.nr; r += 2 * C::kSplit) {
                 float f0, f1;
                 const float L = factors(r, f0, f1), inv = p.whole() ? (L == 0.f ? 0.f : a.c.v_scale / L) : 1.f;
-                float *to = p.whole() ? a.out + row_of[r] : part + r * D;
+                float *to = p.whole() ? a.out + roff[r] : part + r * D;
 #pragma unroll
                 for (int hf = 0; hf < C::kHalves; ++hf) {
                     const int d = 128 * hf + kt;
@@ -770,7 +762,7 @@ __global__ void __launch_bounds__(Cfg<D, NP>::kThreads, 1) attn_paged_tc_kernel(
                 join_parts<D, NP, 32 * kSoftWarps, 1, 4>(a, p, st_id, all_sync, reinterpret_cast<float *>(pbuf), red, flag);
             }
             all_sync();
-            if (lane == 0) mbar_arrive(&q_free[qb]);
+            if (lane == 0) mbar_arrive(q_free);
             ++seg;
         }
     }
@@ -792,29 +784,27 @@ constexpr size_t kMaxSmem = 232448;
 
 }  // namespace
 
-// More than 8 query rows a head over enough keys: rows cost this kernel matrix columns and the other
-// one instructions, but a CTA's first outputs take some 10 us longer here. Measured, the other
-// kernel : this one in us, at rows a head x keys a CTA, 8 heads of K and V:
-//   D = 128   8 x 13800  83 : 114   16 x 1725  27 : 29   16 x 3450  40 : 40   16 x 13800  131 : 118
-//             32 x 430   18 : 25    32 x 860   29 : 29   32 x 1725  42 : 37   32 x 13800  233 : 140
-//   D = 256   8 x 13800  141 : 192  16 x 860   30 : 32   16 x 3450  75 : 65   16 x 13800  271 : 197
-//             32 x 430   27 : 31    32 x 860   50 : 47   64 x 430   42 : 40   64 x 3450   269 : 196
-// which crosses where rows x D x keys a CTA are some 4M. Keys are counted by the page table's width,
+// More than 16 query rows a head of 128 (8 of 256) over enough keys: rows cost this kernel matrix
+// columns and the other one instructions, but a CTA's first outputs take some 10 us longer here.
+// Measured, the other kernel : this one in us, at rows a head x keys a CTA, 8 heads of K and V:
+//   D = 128   16 x 13800  117 : 118  32 x 430   18 : 26    32 x 860   28 : 30   32 x 1725  38 : 38
+//             32 x 3450    63 : 52   32 x 13800 208 : 140  64 x 430   25 : 28   64 x 860   45 : 41
+//   D = 256   8 x 13800   141 : 192  12 x 1725  43 : 42    16 x 860   30 : 32   16 x 3450  73 : 64
+//             16 x 13800  261 : 191  32 x 430   26 : 31    32 x 860   49 : 47   64 x 430   41 : 40
+// which crosses where rows x D x keys a CTA are some 6M. Keys are counted by the page table's width,
 // which is what a launch knows of them.
 PagedTcPlan attn_paged_tc_plan(const df_paged_kv &c, int blk, int nq) {
     const int rows = blk * (nq / c.n_kv_heads), ctas = sm_count() < kOpsCounters ? sm_count() : kOpsCounters;
     const double keys = (double)c.batch * c.n_kv_heads * c.max_pages * c.page_size / ctas;
     PagedTcPlan p{0, ctas};
-    if (rows <= 8 || c.head_dim == 64 || keys * rows * c.head_dim < 4e6) return p;
-    p.np = c.head_dim == 256 || rows <= 16 ? 16 : 32;
-    const size_t fixed = c.head_dim == 256 ? Cfg<256, 16>::kFixed : p.np == 16 ? Cfg<128, 16>::kFixed : Cfg<128, 32>::kFixed;
-    if (fixed + (size_t)(c.batch + 1) * 4 > kMaxSmem) p.np = 0;
+    if (c.head_dim == 64 || rows <= (c.head_dim == 256 ? 8 : 16) || keys * rows * c.head_dim < 6e6) return p;
+    const size_t fixed = c.head_dim == 256 ? Cfg<256, 16>::kFixed : Cfg<128, 32>::kFixed;
+    if (fixed + (size_t)(c.batch + 1) * 4 <= kMaxSmem) p.np = c.head_dim == 256 ? 16 : 32;
     return p;
 }
 
 int launch_attn_paged_tc(const AttnPagedArgs &a, const PagedTcPlan &p, cudaStream_t s) {
-    if (a.c.head_dim == 256) return launch_one<256, 16>(a, p.ctas, s);
-    return p.np == 16 ? launch_one<128, 16>(a, p.ctas, s) : launch_one<128, 32>(a, p.ctas, s);
+    return a.c.head_dim == 256 ? launch_one<256, 16>(a, p.ctas, s) : launch_one<128, 32>(a, p.ctas, s);
 }
 
 }  // namespace df

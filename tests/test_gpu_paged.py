@@ -364,7 +364,8 @@ ATTEND = [
 ]
 
 
-# (more than 8 rows a head of 128 or 256, which the kernel for long contexts takes)
+# (more than 8 rows a head of 128 or 256; the kernel for long contexts takes those of 256 and
+# more than 16 of 128)
 LONG = [
     ([64], [5], 5, 4, 2, 128, 16, False),
     ([0], [9], 9, 2, 2, 128, 16, True),
@@ -498,7 +499,7 @@ def test_attention_bad_tables_and_lengths_reach_the_status(shape):
 
 
 @pytest.mark.parametrize("d,nq,batch,long", [(64, 2, 2048, False), (128, 8, 2048, False), (256, 4, 2048, False),
-                                             (256, 16, 2048, False), (128, 24, 1500, True), (256, 24, 1100, True)])
+                                             (256, 16, 2048, False), (128, 40, 1500, True), (256, 24, 1100, True)])
 def test_attention_of_the_largest_batch(d, nq, batch, long):
     # sequences of 0 to 5 cached rows and one new one, a page each
     rng = np.random.default_rng(31)
