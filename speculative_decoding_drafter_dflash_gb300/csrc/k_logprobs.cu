@@ -54,6 +54,12 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     return r;
 }
 
+// The F32 value above v (not NaN, not +inf).
+__device__ __forceinline__ float above(float v) {
+    const int b = __float_as_int(v);
+    return __int_as_float(b == (int)0x80000000 || b == 0 ? 1 : (b > 0 ? b + 1 : b - 1));
+}
+
 __device__ __forceinline__ bool better(float av, int ai, float bv, int bi) {
     return av > bv || (av == bv && ai < bi);
 }
@@ -218,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const __gri
     st.mu = -INFINITY;
     st.S = st.U = 0.f;
     float2 S2 = make_float2(0.f, 0.f), U2 = make_float2(0.f, 0.f);
-    float tau = -INFINITY;                   // entries to list are larger (later indices lose ties)
+    float thr = -INFINITY;                   // entries to list are at least this
     int held = 0;
     // The reference follows the maximum m of what comes when the exponents could overflow.
     auto follow = [&](float m) {
@@ -231,7 +237,8 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const __gri
             st.rebase(m, c);
         }
     };
-    // The CTA's list takes what the warps hold, in warp order; tau becomes its last value.
+    // The CTA's list takes what the warps hold, in warp order; thr becomes the value above
+    // its last (later indices lose ties).
     auto collect = [&]() {
         if (warp != 0) {
             slv[warp][lane] = st.lv;
@@ -278,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const __gri
             if (lane == 0) top_s = st.lv;
         }
         __syncthreads();
-        tau = tau_s;
+        thr = above(tau_s);
     };
     auto unpack = [](const Raw<BF16> &q, float (&x)[kPerLane]) {
 #pragma unroll
@@ -337,6 +344,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const __gri
         }
         tau0 = fmaxf(any, every);
     }
+    thr = tau0;
     const int steps = end > begin ? (end - begin + kRowsOfStep - 1) / kRowsOfStep : 0;
     for (int it = 0, due = 1; it < steps; ++it) {
         if (it == due) {
@@ -348,38 +356,34 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const __gri
         float x[kPerLane];
         unpack(next, x);
         if (j + kRowsOfStep < end) next = load<BF16>(base, j + kRowsOfStep, mis, end);
-        float gm[4];                         // of every four
-#pragma unroll
-        for (int k = 0; k < 4; ++k) gm[k] = fmaxf(fmaxf(x[4 * k], x[4 * k + 1]), fmaxf(x[4 * k + 2], x[4 * k + 3]));
-        const float bm = fmaxf(fmaxf(gm[0], gm[1]), fmaxf(gm[2], gm[3]));
-        const bool want = (it == 0 ? bm >= tau0 : bm > tau) || (bm - st.mu) * c > 60.f;
+        const float bm = largest(x);
+        const bool want = bm >= thr || (bm - st.mu) * c > 60.f;
         if (__any_sync(0xffffffffu, want)) {
             if (__any_sync(0xffffffffu, st.mu == -INFINITY || (bm - st.mu) * c > 60.f)) follow(warp_max(bm));
             // What a held entry leaves in the step: nothing in the sums.
             const float at0 = st.mu == -INFINITY ? 0.f : st.mu, out = at0 - fmaxf(1000.f / c, fabsf(at0));
+            unsigned hits = 0;
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              if (!__any_sync(0xffffffffu, it == 0 ? gm[g] >= tau0 : gm[g] > tau)) continue;
+            for (int k = 0; k < kPerLane; ++k) hits |= x[k] >= thr ? 1u << k : 0u;
+            auto index = [&](int k) { return j + ((k / E) * 32 + lane) * E + k % E - mis; };
+            if (thr == -INFINITY)            // (places outside the row are -inf too)
+                for (int k = 0; k < kPerLane; ++k)
+                    if (index(k) < 0 || index(k) >= end - mis) hits &= ~(1u << k);
+            // Entries are few: one a lane at a time, picked out of the registers.
+            for (unsigned some; (some = __ballot_sync(0xffffffffu, hits != 0)) != 0; held += __popc(some)) {
+                const unsigned low = hits & (0u - hits);
+                float v = x[0];
 #pragma unroll
-              for (int k = 4 * g; k < 4 * g + 4; ++k) {
-                bool p = it == 0 ? x[k] >= tau0 : x[k] > tau;
-                unsigned bal = __ballot_sync(0xffffffffu, p);
-                if (bal) {
-                    const int idx = j + ((k / E) * 32 + lane) * E + k % E - mis;
-                    if (it == 0 && tau0 == -INFINITY) {      // (places outside the row are -inf too)
-                        p = p && idx >= 0 && idx < end - mis;
-                        bal = __ballot_sync(0xffffffffu, p);
-                    }
-                    if (p) {
-                        const int at = held + __popc(bal & ((1u << lane) - 1));
-                        held_v[warp][at] = x[k];
-                        held_i[warp][at] = idx;
-                        x[k] = out;
-                    }
-                    held += __popc(bal);
+                for (int k = 1; k < kPerLane; ++k) v = low & (1u << k) ? x[k] : v;
+                if (hits) {
+                    const int at = held + __popc(some & ((1u << lane) - 1));
+                    held_v[warp][at] = v;
+                    held_i[warp][at] = index(__ffs(hits) - 1);
+                    hits &= hits - 1;
                 }
-              }
             }
+#pragma unroll
+            for (int k = 0; k < kPerLane; ++k) x[k] = x[k] >= thr ? out : x[k];
             // Far more than expected (ties, rising rows): the warp's own list takes them.
             while (held >= 32) {
                 __syncwarp();
@@ -387,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const __gri
                 st.take(held_v[warp][held + lane], held_i[warp][held + lane], kp, c);
                 __syncwarp();
                 if (__shfl_sync(0xffffffffu, st.li, kp - 1) != kNone)
-                    tau = fmaxf(tau, __shfl_sync(0xffffffffu, st.lv, kp - 1));
+                    thr = fmaxf(thr, above(__shfl_sync(0xffffffffu, st.lv, kp - 1)));
             }
         }
         const float ref = st.mu == -INFINITY ? 0.f : st.mu;
