@@ -185,13 +185,14 @@ __device__ __forceinline__ Raw<BF16> load(const uint8_t *base, int j, int mis, i
 
 // CTA (chunk, row). Bound: the logits, read once; per logit one conversion (16-bit), a running
 // maximum, half of three packed F32 operations, two single ones and the exponential.
-// 1024 rows of 248320 bf16 values with 20 alternatives: 140 us for 509 MB, 3.6 TB/s of the copy's 6.8, 117 us
+// 1024 rows of 248320 bf16 values with 20 alternatives: 131 us for 509 MB, 3.9 TB/s of the copy's 6.8, 109 us
 // with none; a row a CTA, four CTAs an SM, so 1024 rows are two rounds of 608, the second a third empty,
-// and 63% of the issue slots are taken. The list costs the difference: a step that may hold an entry
-// is looked through (30% of them), and the list is brought together five times a row. One row of
-// 248320 F32 values over 61 CTAs: 8.9 us, 16 rows of 262144: 15.6 us, the latencies of a step or two, a
+// and 62% of the issue slots are taken. The list costs the difference: a step that may hold an entry
+// is looked through (23% of them), and the list is brought together five times a row. One row of
+// 248320 F32 values over 61 CTAs: 8.3 us, 16 rows of 262144: 14.9 us, the latencies of a step or two, a
 // sort, the arrival and the join. (Two or three steps read ahead: 138 to 240 us; 7 CTAs of 4 warps an
-// SM, all rows at once: 222 us; entries ranked by all warps instead of sorted by one: 176 us, of spills.)
+// SM, all rows at once: 222 us; entries ranked by all warps instead of sorted by one: 176 us, of spills;
+// entries looked for one ballot a value: 140 us, read again from memory: 165 us.)
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const __grid_constant__ LogprobsArgs a,
                                                                   int chunk, int n_chunks, float c) {
